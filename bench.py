@@ -47,7 +47,7 @@ HBM_PEAK_GBS = 8000.0  # MI355X HBM3E, vendor figure
 # record, the launch-size limits).  Recorded counters stay valid while the
 # code (not the comments) of these files is unchanged.
 KERNEL_SOURCES = [os.path.join(ROOT, "sharded_optimizer_step_shard_amd", "csrc", f)
-                  for f in ("zero_kernels.hip", "zero_internal.h", "zero_chunks.cpp")] + \
+                  for f in ("zero_kernels.hip", "zero_device.h", "zero_internal.h", "zero_chunks.cpp")] + \
                  [os.path.join(ROOT, "include", "zero_shard.h")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic.json")
 

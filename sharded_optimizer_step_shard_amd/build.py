@@ -4,8 +4,7 @@
 
 (run as a script: importing the package needs the library already built).
 
-compiles csrc/zero_kernels.hip, csrc/zero_probes.hip, csrc/zero_chunks.cpp and
-csrc/zero_api.cpp for gfx950 with hipcc.
+compiles the sources in csrc/ for gfx950 with hipcc, side by side, and links them.
 Flags that matter for the results:
   -ffp-contract=off  no fused multiply-add: the double arithmetic of the step
                      must be the separately rounded operations it is defined as.
@@ -17,6 +16,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,7 +27,7 @@ LIB = os.path.join(PKG, "libzero_shard.so")
 ARCH = os.environ.get("ZERO_SHARD_ARCH", "gfx950")
 
 HIP_FLAGS = [
-    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-shared",
+    f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fno-fast-math",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall", "-Wno-unused-command-line-argument",
@@ -40,13 +41,22 @@ def hipcc() -> str:
     return "hipcc"
 
 
+SOURCES = ("zero_kernels.hip", "zero_probes.hip", "zero_chunks.cpp", "zero_api.cpp")
+
+
 def build(verbose: bool = True, out: str = LIB, extra=()) -> str:
-    srcs = [os.path.join(CSRC, f)
-            for f in ("zero_kernels.hip", "zero_probes.hip", "zero_chunks.cpp", "zero_api.cpp")]
-    cmd = [hipcc(), *HIP_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-o", out, *srcs]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+    flags = [*HIP_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC]
+    with tempfile.TemporaryDirectory() as tmp:
+        objs = [os.path.join(tmp, f + ".o") for f in SOURCES]
+        cmds = [[hipcc(), *flags, "-c", "-o", o, os.path.join(CSRC, f)]
+                for o, f in zip(objs, SOURCES)]
+        link = [hipcc(), *flags, "-shared", "-o", out, *objs]
+        if verbose:
+            for cmd in (*cmds, link):
+                print(" ".join(cmd), flush=True)
+        with ThreadPoolExecutor(len(cmds)) as pool:
+            list(pool.map(lambda c: subprocess.run(c, check=True), cmds))
+        subprocess.run(link, check=True)
     return out
 
 
