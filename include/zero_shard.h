@@ -29,6 +29,12 @@
  * per gradient bucket) and zero_shard_step_scheduled (step constants read
  * from device memory, for steps captured in a HIP graph).
  *
+ * Clipping by the global gradient norm: zero_reduce_norm_shard (the reduce,
+ * with the shard's sum of squares in the same pass), zero_clip_coef (the
+ * coefficient from every rank's square) and a _clipped form of each step;
+ * zero_norm_pieces and zero_scale_pieces do the same for gradients that are
+ * many tensors instead of a shard.
+ *
  * Arithmetic, fixed so that every result is reproducible bit for bit:
  *   - g: the partials are widened exactly to double and summed in double,
  *     rank 0 first, ranks 1..N-1 in order; the sum is divided by N in
@@ -43,7 +49,8 @@
  *     and b^t = pow(b, t) are formed in double.
  *   - the bf16 parameter is theta' (fp32) rounded to nearest even; NaN
  *     stays NaN with its sign and the quiet bit set; overflow gives inf.
- *   Non-finite inputs propagate per IEEE; there is no clipping or skipping.
+ *   Non-finite inputs propagate per IEEE; only the _clipped steps clip, and
+ *   only they skip (a step whose global norm is not finite).
  *
  * Conventions for every entry point:
  *   - All array arguments are device pointers unless stated otherwise.
@@ -92,10 +99,11 @@
 extern "C" {
 #endif
 
-/* Element type of the gradient partials. */
+/* Element type of the gradient partials, or of a tensor's piece. */
 typedef enum zero_dtype {
     ZERO_BF16 = 0,   /* bfloat16, passed as 16-bit patterns */
-    ZERO_FP32 = 1    /* IEEE binary32 (gradients communicated in fp32) */
+    ZERO_FP32 = 1,   /* IEEE binary32 (gradients communicated in fp32) */
+    ZERO_FP16 = 2    /* IEEE binary16; pieces only, UNSUPPORTED for partials */
 } zero_dtype;
 
 /* AdamW hyper-parameters, in double.  `step` is t >= 1, the number of this
@@ -133,6 +141,31 @@ typedef struct zero_chunk {
     int64_t tensor_off;  /* element offset of shard_off inside that tensor */
 } zero_chunk;
 
+/* One piece of a tensor, for the calls over many tensors: elements
+ * src[0 .. len) and the place dst[0 .. len) of their scaled values (dst ==
+ * src: in place).  32 bytes.  Built on the host by zero_build_pieces; the
+ * caller copies the table to device memory. */
+typedef struct zero_piece {
+    const void *src;
+    void *dst;
+    int32_t len;             /* element count, 0 .. max_piece (0: an empty tensor) */
+    int32_t tensor_id;
+    int32_t tensor_pieces;   /* first piece of a tensor: how many it has; else 0 */
+    int16_t src_dt, dst_dt;  /* zero_dtype of each side */
+} zero_piece;
+
+/* What the clipping coefficient is formed with.  Host struct; `out` is a
+ * device array of two doubles, 16-byte aligned: out[0] = norm, out[1] = coef
+ * (see zero_clip_coef).
+ * Requirements: max_norm >= 0 (INFINITY: never clip), finite eps >= 0, finite
+ * inv_scale > 0. */
+typedef struct zero_clip_spec {
+    double max_norm;
+    double eps;         /* added to the norm in the quotient, 1e-6 by custom */
+    double inv_scale;   /* 1 / the loss scale the gradients carry; 1 without one */
+    double *out;
+} zero_clip_spec;
+
 /* Return codes. */
 enum {
     ZERO_OK = 0,
@@ -141,7 +174,7 @@ enum {
     ZERO_ERR_UNSUPPORTED = 3,  /* unknown dtype */
     ZERO_ERR_ALIAS = 4,        /* an input array overlaps an array the call writes */
     ZERO_ERR_HIP = 5,          /* the HIP runtime reported an error at launch */
-    ZERO_ERR_CAPACITY = 6,     /* caller's chunk array too small (see n_out) */
+    ZERO_ERR_CAPACITY = 6,     /* caller's table or workspace too small */
     ZERO_ERR_NOT_DEVICE = 7    /* an array range is not (wholly) device memory */
 };
 
@@ -162,6 +195,12 @@ enum {
  * the same bits either way. */
 #define ZERO_SMALL_LAUNCH_CHUNKS 2048
 #define ZERO_SMALL_LAUNCH_CHUNKS_12B 16384
+/* Chunk length for the clipped steps on a reduced fp32 gradient (n_ranks = 1,
+ * ZERO_FP32), and piece length for the calls over many tensors. */
+#define ZERO_DEFAULT_MAX_CHUNK_REDUCED 1024
+#define ZERO_DEFAULT_MAX_PIECE 16384
+/* Partial sums zero_reduce_norm_shard leaves in its workspace, at most. */
+#define ZERO_NORM_PARTIALS 16384
 
 /*
  * Shard geometry and the chunk table (host only; no device calls).
@@ -465,6 +504,171 @@ int zero_adamw_shard(const float *grad, float *master, float *m, float *v, int64
  */
 int zero_gather_write(const float *master, int64_t shard_len, const zero_chunk *d_chunks,
                       int64_t n_chunks, hipStream_t stream);
+
+/*
+ * Clipping by the global norm: the gradient of the whole model is scaled by
+ * min(1, max_norm / norm) before the update, so the norm of every rank's shard
+ * has to be known before any element is updated.  A clipped step is
+ *
+ *   zero_reduce_norm_shard   g = mean of the partials, and sum g^2
+ *   (all-gather of one double a rank, by the caller)
+ *   zero_clip_coef           norm and coefficient, on the device
+ *   zero_shard_step_clipped  from g: partials = {g}, n_ranks = 1, ZERO_FP32
+ *
+ * with no value read back by the host.  The gradients are averaged over the
+ * ranks before they are clipped, since the full-batch gradient is their mean
+ * ("并行策略总览：六个维度各切什么、怎么通信", data-parallel section), and each rank
+ * clips the segment it owns ("CS336 2026 Lecture 8: Parallelism Basics",
+ * Slides 19-20).
+ *
+ * Sums of squares are formed in double from exact squares (an fp32 value
+ * squared is exact in double) in an order fixed by the element count or the
+ * table, so the same call gives the same bits every time.
+ *
+ * Workspace: device memory, 16-byte aligned, zero_norm_workspace(n_pieces)
+ * bytes (n_pieces = 0 is enough for zero_reduce_norm_shard).  Its content
+ * means nothing between calls and needs no initialisation.  Calls that may
+ * run at the same time (other streams, graphs replayed side by side) need a
+ * workspace each.
+ */
+int64_t zero_norm_workspace(int64_t n_pieces);   /* -1 for n_pieces outside [0, INT32_MAX] */
+
+/*
+ * zero_reduce_shard with the sum of squares in the same pass:
+ *   g[i] = fp32(((acc[i] if acc) + two-level sum) / (n_ranks * micro_batches)),
+ *   *sq  = sum over i < n of g[i]^2  (device double, 8-byte aligned).
+ * g goes to grad_out unless that is NULL (the norm alone: the step then reduces
+ * the partials again).  With partials of b bytes an element and n_ranks = N, a
+ * clipped step moves N b + 8 bytes an element besides the state when g is kept
+ * and 2 N b when it is not: keep it from N b = 8 on.
+ * rs: as zero_shard_step_ex; NULL for the flat order and one micro-batch.
+ * grad_out may be rs->acc itself, and must not overlap it otherwise.
+ * spec: not NULL to form the coefficient too, as zero_clip_coef does from this
+ * square alone (a job of one shard).
+ * n == 0 (an empty shard) gives *sq = 0.
+ * Errors: INVALID as zero_reduce_shard and zero_shard_step_ex, and for a NULL
+ * sq, a NULL workspace, or a bad spec; CAPACITY for a small workspace
+ * (checked with the counts); MISALIGNED; UNSUPPORTED; ALIAS when anything
+ * written (grad_out, sq, spec->out, workspace) overlaps an input or another
+ * output; NOT_DEVICE; HIP.
+ */
+int zero_reduce_norm_shard(const void *const *partials, int n_ranks, int gdt,
+                           const zero_reduce_spec *rs, int64_t n, float *grad_out, double *sq,
+                           const zero_clip_spec *spec, void *workspace, int64_t workspace_bytes,
+                           hipStream_t stream);
+
+/*
+ * The clipping coefficient, on the device, from n_sq sums of squares (one a
+ * rank, all-gathered, or of several groups of tensors):
+ *   norm = inv_scale * sqrt(sq[0] + ... + sq[n_sq - 1])    -> spec->out[0]
+ *   coef = inv_scale * min(1, max_norm / (norm + eps))     -> spec->out[1]
+ * in double, the squares added in a fixed order.  coef takes the loss scale
+ * out too.  Exactly inv_scale where norm + eps <= max_norm.  If the sum of
+ * squares is not finite, coef is NaN, and the calls that take it change
+ * nothing: a step with an overflowed gradient is skipped on every rank alike.
+ * Errors: INVALID (NULL sq or spec, n_sq outside [1, INT32_MAX], a bad spec),
+ * MISALIGNED (sq 8, spec->out 16 bytes), ALIAS (spec->out overlaps sq),
+ * NOT_DEVICE, HIP.
+ */
+int zero_clip_coef(const double *sq, int64_t n_sq, const zero_clip_spec *spec, hipStream_t stream);
+
+/*
+ * The clipped steps: as the step each is named after, on the gradient
+ *   g'[i] = fp32(coef * g[i]),  coef = clip[1],
+ * with g the fp32 reduced gradient and clip the two doubles that a
+ * zero_clip_spec's out received (device, 16-byte aligned), read when the
+ * kernel runs.  Equal, bit for bit, to scaling the reduced gradient by
+ * zero_scale_pieces and stepping from that; with coef = 1 to the step that
+ * does not clip.  With a NaN coef nothing is changed.  From a reduced gradient
+ * pass partials = {g}, n_ranks = 1 and ZERO_FP32, and cut the chunks by
+ * ZERO_DEFAULT_MAX_CHUNK_REDUCED.  Errors as the step they are named after, with
+ * clip treated as that step's state arrays are (ALIAS when it overlaps them).
+ * In a scheduled step zero_step_index_advance counts a skipped step too.
+ */
+int zero_shard_step_clipped(const void *const *partials, int n_ranks, int gdt,
+                            float *master, float *m, float *v, int64_t shard_len,
+                            const zero_chunk *d_chunks, int64_t n_chunks,
+                            const zero_adamw_hparams *hp, const double *clip, hipStream_t stream);
+int zero_shard_step_bf16_moments_clipped(const void *const *partials, int n_ranks, int gdt,
+                                         float *master, uint16_t *m, uint16_t *v, int64_t shard_len,
+                                         const zero_chunk *d_chunks, int64_t n_chunks,
+                                         const zero_adamw_hparams *hp, const double *clip,
+                                         hipStream_t stream);
+int zero_shard_step_kahan_clipped(const void *const *partials, int n_ranks, int gdt,
+                                  uint16_t *comp, uint16_t *m, uint16_t *v, int64_t shard_len,
+                                  const zero_chunk *d_chunks, int64_t n_chunks,
+                                  const zero_adamw_hparams *hp, const double *clip,
+                                  hipStream_t stream);
+int zero_shard_step_scheduled_clipped(const void *const *partials, int n_ranks, int gdt,
+                                      float *master, float *m, float *v, int64_t shard_len,
+                                      const zero_chunk *d_chunks, int64_t n_chunks,
+                                      const zero_step_consts *consts, int64_t n_consts,
+                                      const int64_t *index, const double *clip, hipStream_t stream);
+int zero_shard_step_bf16_moments_scheduled_clipped(const void *const *partials, int n_ranks, int gdt,
+                                                   float *master, uint16_t *m, uint16_t *v,
+                                                   int64_t shard_len, const zero_chunk *d_chunks,
+                                                   int64_t n_chunks, const zero_step_consts *consts,
+                                                   int64_t n_consts, const int64_t *index,
+                                                   const double *clip, hipStream_t stream);
+int zero_shard_step_kahan_scheduled_clipped(const void *const *partials, int n_ranks, int gdt,
+                                            uint16_t *comp, uint16_t *m, uint16_t *v,
+                                            int64_t shard_len, const zero_chunk *d_chunks,
+                                            int64_t n_chunks, const zero_step_consts *consts,
+                                            int64_t n_consts, const int64_t *index,
+                                            const double *clip, hipStream_t stream);
+
+/*
+ * The table of pieces of many tensors (host only; no device calls, nothing
+ * dereferenced on the device).
+ *
+ * src, src_dt, numels: host arrays of n_tensors device addresses, zero_dtype
+ * values and element counts; tensor t is numels[t] elements back to back at
+ * src[t], at any address its element size divides.
+ * dst, dst_dt: where zero_scale_pieces puts each tensor, and in which type;
+ * both NULL for in place (zero_norm_pieces writes neither way).
+ * Tensors are cut every max_piece elements (a positive multiple of 64, at most
+ * 2^24), the first piece shorter so that the others start 16-byte aligned in
+ * dst; an empty tensor has one piece of length 0.  A contiguous run of the table that ends where a
+ * tensor ends may be passed alone.
+ * out, cap, n_out: as zero_build_chunks.
+ * Errors: INVALID (a NULL array, n_tensors < 0, a negative count or a total
+ * above ZERO_MAX_LEN, a NULL address of a non-empty tensor, one of dst and
+ * dst_dt NULL, a bad max_piece), MISALIGNED (an address its element size does
+ * not divide), UNSUPPORTED (a type), ALIAS (a tensor's place overlaps another's
+ * place or any tensor, unless it is exactly its own tensor in its own type),
+ * CAPACITY.
+ */
+int zero_build_pieces(const void *const *src, const int *src_dt, void *const *dst,
+                      const int *dst_dt, const int64_t *numels, int n_tensors, int64_t max_piece,
+                      zero_piece *out, int64_t cap, int64_t *n_out);
+
+/*
+ * Sums of squares of many tensors: *sq = sum over all pieces (device double),
+ * and, unless tensor_sq is NULL, tensor_sq[t] = sum over tensor t's (device,
+ * n_tensors doubles; a tensor_id outside [0, n_tensors) is counted in *sq
+ * alone).  Both are of the elements as they are: inv_scale enters the norm.
+ * spec: not NULL to form norm and coefficient too, as zero_clip_coef.
+ * An empty table gives *sq = 0.  Pieces with a NULL src, a length outside
+ * [0, 2^24] or an unknown type count as empty; the addresses in the table
+ * are otherwise trusted.
+ * Errors: INVALID (NULL sq or workspace, a NULL table of n_pieces > 0, n_pieces
+ * or n_tensors outside [0, INT32_MAX], a bad spec), CAPACITY (workspace),
+ * MISALIGNED, ALIAS (outputs, workspace and table overlap), NOT_DEVICE, HIP.
+ */
+int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, double *tensor_sq,
+                     int64_t n_tensors, const zero_clip_spec *spec, void *workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * dst[j] = dst_dt(coef * src[j]) for every piece, coef = clip[1] (device, as
+ * for the clipped steps): the product in double, rounded once to nearest even.
+ * With a NaN coef nothing is written; with coef = 1 pieces in place are not
+ * touched (they are what they would be).
+ * Errors: INVALID (NULL clip, a NULL table of n_pieces > 0, n_pieces outside
+ * [0, INT32_MAX]), MISALIGNED, NOT_DEVICE, HIP.
+ */
+int zero_scale_pieces(const zero_piece *d_pieces, int64_t n_pieces, const double *clip,
+                      hipStream_t stream);
 
 /* Static description of a return code. */
 const char *zero_strerror(int code);

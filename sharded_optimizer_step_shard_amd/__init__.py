@@ -24,6 +24,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libzero_shard.so")
 
 ZERO_BF16, ZERO_FP32 = 0, 1
+ZERO_FP16 = 2                   # pieces of tensors only
 ZERO_OK, ZERO_ERR_INVALID, ZERO_ERR_MISALIGNED, ZERO_ERR_UNSUPPORTED = 0, 1, 2, 3
 ZERO_ERR_ALIAS, ZERO_ERR_HIP, ZERO_ERR_CAPACITY, ZERO_ERR_NOT_DEVICE = 4, 5, 6, 7
 ZERO_MAX_RANKS = 64
@@ -33,12 +34,21 @@ ZERO_DEFAULT_MAX_CHUNK_FP32 = 1024   # fp32 partials
 # step launches up to this many chunks run at a higher occupancy
 ZERO_SMALL_LAUNCH_CHUNKS = 2048        # 16-byte and extended steps
 ZERO_SMALL_LAUNCH_CHUNKS_12B = 16384   # 12-byte step
+ZERO_DEFAULT_MAX_CHUNK_REDUCED = 1024  # clipped steps on a reduced fp32 gradient
+ZERO_DEFAULT_MAX_PIECE = 16384         # calls over many tensors
+ZERO_NORM_PARTIALS = 16384
 ZERO_PROBE_SUM_MAX = 16
 
 # Mirrors `zero_chunk` (32 bytes).
 CHUNK_DTYPE = np.dtype([("shard_off", "<i8"), ("dst", "<u8"), ("len", "<i4"),
                         ("tensor_id", "<i4"), ("tensor_off", "<i8")], align=True)
 assert CHUNK_DTYPE.itemsize == 32
+
+
+# Mirrors `zero_piece` (32 bytes).
+PIECE_DTYPE = np.dtype([("src", "<u8"), ("dst", "<u8"), ("len", "<i4"), ("tensor_id", "<i4"),
+                        ("tensor_pieces", "<i4"), ("src_dt", "<i2"), ("dst_dt", "<i2")], align=True)
+assert PIECE_DTYPE.itemsize == 32
 
 
 class HParams(ctypes.Structure):
@@ -63,6 +73,12 @@ class ReduceSpec(ctypes.Structure):
     """Mirrors `zero_reduce_spec`."""
     _fields_ = [("group", ctypes.c_int32), ("micro_batches", ctypes.c_int32),
                 ("acc", ctypes.c_void_p)]
+
+
+class ClipSpec(ctypes.Structure):
+    """Mirrors `zero_clip_spec`."""
+    _fields_ = [("max_norm", ctypes.c_double), ("eps", ctypes.c_double),
+                ("inv_scale", ctypes.c_double), ("out", ctypes.c_void_p)]
 
 
 class ZeroShardError(RuntimeError):
@@ -104,6 +120,21 @@ _lib.zero_shard_step_bf16_moments_scheduled.argtypes = _lib.zero_shard_step_sche
 _lib.zero_shard_step_kahan_scheduled.argtypes = _lib.zero_shard_step_scheduled.argtypes
 _lib.zero_step_index_advance.argtypes = [_vp, _i64, _vp]
 _lib.zero_check_chunks.argtypes = [_vp, _i64, _i64, _vp, _vp, _i32]
+_lib.zero_norm_workspace.argtypes = [_i64]
+_lib.zero_norm_workspace.restype = _i64
+_lib.zero_reduce_norm_shard.argtypes = [_vp, _i32, _i32, ctypes.POINTER(ReduceSpec), _i64, _vp, _vp,
+                                        ctypes.POINTER(ClipSpec), _vp, _i64, _vp]
+_lib.zero_clip_coef.argtypes = [_vp, _i64, ctypes.POINTER(ClipSpec), _vp]
+_lib.zero_build_pieces.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i64,
+                                   ctypes.POINTER(_i64)]
+_lib.zero_norm_pieces.argtypes = [_vp, _i64, _vp, _vp, _i64, ctypes.POINTER(ClipSpec), _vp, _i64, _vp]
+_lib.zero_scale_pieces.argtypes = [_vp, _i64, _vp, _vp]
+for _f in ("zero_shard_step", "zero_shard_step_bf16_moments", "zero_shard_step_kahan",
+           "zero_shard_step_scheduled", "zero_shard_step_bf16_moments_scheduled",
+           "zero_shard_step_kahan_scheduled"):
+    # the clipped form takes the coefficient before the stream
+    getattr(_lib, _f + "_clipped").argtypes = [*getattr(_lib, _f).argtypes[:-1], _vp, _vp]
+    getattr(_lib, _f + "_clipped").restype = _i32
 _lib.zero_strerror.argtypes = [_i32]
 _lib.zero_strerror.restype = ctypes.c_char_p
 for _f in ("zero_build_chunks", "zero_shard_step", "zero_reduce_shard", "zero_adamw_shard",
@@ -112,7 +143,9 @@ for _f in ("zero_build_chunks", "zero_shard_step", "zero_reduce_shard", "zero_ad
            "zero_accumulate_shard", "zero_shard_step_bf16_moments", "zero_shard_step_kahan",
            "zero_shard_step_buckets", "zero_make_step_consts", "zero_shard_step_scheduled",
            "zero_step_index_advance", "zero_shard_step_bf16_moments_scheduled",
-           "zero_shard_step_kahan_scheduled", "zero_check_chunks", "zero_probe_sum"):
+           "zero_shard_step_kahan_scheduled", "zero_check_chunks", "zero_probe_sum",
+           "zero_reduce_norm_shard", "zero_clip_coef", "zero_build_pieces", "zero_norm_pieces",
+           "zero_scale_pieces"):
     getattr(_lib, _f).restype = _i32
 
 Ptr = Union[int, "torch.Tensor", None]  # noqa: F821
@@ -222,6 +255,179 @@ def chunks_to_device(table: np.ndarray, device: str = "cuda"):
 def _partial_array(partials):
     addrs = [_addr(p) for p in partials]
     return (ctypes.c_void_p * max(len(addrs), 1))(*addrs)
+
+
+def clip_spec(out: Ptr, max_norm: float, eps: float = 1e-6, inv_scale: float = 1.0) -> ClipSpec:
+    """What the clipping coefficient is formed with; `out` (two doubles on the
+    device) receives the norm and the coefficient.  The caller keeps `out`
+    alive while calls use the spec, as with every array."""
+    return ClipSpec(max_norm, eps, inv_scale, _addr(out))
+
+
+def zero_norm_workspace(n_pieces: int = 0) -> int:
+    """Bytes of workspace for zero_norm_pieces over n_pieces; 0 for
+    zero_reduce_norm_shard."""
+    n = _lib.zero_norm_workspace(n_pieces)
+    if n < 0:
+        raise ZeroShardError(ZERO_ERR_INVALID, "zero_norm_workspace")
+    return n
+
+
+def _spec(spec: Optional[ClipSpec]):
+    return None if spec is None else ctypes.byref(spec)
+
+
+def zero_reduce_norm_shard(partials: Sequence[Ptr], n: int, sq: Ptr, workspace,
+                           grad_out: Ptr = None, group: int = 0, micro_batches: int = 1,
+                           acc: Ptr = None, spec: Optional[ClipSpec] = None,
+                           gdt: Optional[int] = None, stream=None) -> None:
+    """Reduced gradient (to grad_out, unless None) and its sum of squares in
+    one pass; workspace: a tensor or an (address, bytes) pair."""
+    gdt = _gdt_of(partials) if gdt is None else gdt
+    rs = ReduceSpec(group, micro_batches, _addr(acc))
+    ws, ws_bytes = _byte_range(workspace)
+    _check(_lib.zero_reduce_norm_shard(_partial_array(partials), len(partials), gdt,
+                                       ctypes.byref(rs), n, _addr(grad_out), _addr(sq), _spec(spec),
+                                       ws, ws_bytes, _stream(stream)), "zero_reduce_norm_shard")
+
+
+def zero_clip_coef(sq: Ptr, n_sq: int, spec: ClipSpec, stream=None) -> None:
+    """Norm and coefficient of n_sq sums of squares, into the spec's out."""
+    _check(_lib.zero_clip_coef(_addr(sq), n_sq, _spec(spec), _stream(stream)), "zero_clip_coef")
+
+
+def _dense_addr(t) -> int:
+    """Address of a tensor whose elements fill one range of device memory, in
+    any order of its dimensions (permuted tensors included)."""
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live in device memory")
+    if not t.is_contiguous():
+        expect = 1
+        for st, size in sorted((st, size) for st, size in zip(t.stride(), t.shape) if size != 1):
+            if st != expect:
+                raise ValueError("a tensor must fill one range of memory: it has gaps or overlaps")
+            expect *= size
+    return t.data_ptr()
+
+
+def _piece_dt(t) -> int:
+    import torch
+    dt = {torch.bfloat16: ZERO_BF16, torch.float32: ZERO_FP32, torch.float16: ZERO_FP16}.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported tensor dtype {t.dtype}")
+    return dt
+
+
+def zero_build_pieces(tensors: Sequence["torch.Tensor"],  # noqa: F821
+                      dst: Optional[Sequence["torch.Tensor"]] = None,  # noqa: F821
+                      max_piece: int = ZERO_DEFAULT_MAX_PIECE) -> np.ndarray:
+    """Host table (PIECE_DTYPE) of the tensors' pieces; dst: the tensors that
+    zero_scale_pieces writes, in any of the types (None: in place).  The table
+    holds addresses: it stands for as long as the tensors keep their memory."""
+    n = len(tensors)
+    src_a = np.array([_dense_addr(t) for t in tensors], dtype=np.uint64)
+    src_dt = np.array([_piece_dt(t) for t in tensors], dtype=np.int32)
+    numels = np.array([t.numel() for t in tensors], dtype=np.int64)
+    dst_a = dst_dt = None
+    if dst is not None:
+        if len(dst) != n or any(d.shape != t.shape or (d.stride() != t.stride() and not
+                                (d.is_contiguous() and t.is_contiguous()))
+                                for d, t in zip(dst, tensors)):
+            raise ValueError("dst must match the tensors in number, shape and strides")
+        dst_a = np.array([_dense_addr(t) for t in dst], dtype=np.uint64)
+        dst_dt = np.array([_piece_dt(t) for t in dst], dtype=np.int32)
+    args = (src_a.ctypes.data, src_dt.ctypes.data, None if dst is None else dst_a.ctypes.data,
+            None if dst is None else dst_dt.ctypes.data, numels.ctypes.data, n, max_piece)
+    count = _i64(0)
+    _check(_lib.zero_build_pieces(*args, None, 0, ctypes.byref(count)), "zero_build_pieces")
+    out = np.zeros(count.value, dtype=PIECE_DTYPE)
+    if count.value:
+        _check(_lib.zero_build_pieces(*args, out.ctypes.data, count.value, ctypes.byref(count)),
+               "zero_build_pieces")
+    return out
+
+
+def pieces_to_device(table: np.ndarray, device: str = "cuda"):
+    """Copy a host table of pieces into a device buffer (torch owns the memory)."""
+    return chunks_to_device(table, device)
+
+
+def zero_norm_pieces(d_pieces: Ptr, n_pieces: int, sq: Ptr, workspace, tensor_sq=None,
+                     spec: Optional[ClipSpec] = None, stream=None) -> None:
+    """Sum of squares of many tensors into sq, each tensor's into tensor_sq
+    (a float64 tensor, one element a tensor), and the coefficient if spec."""
+    ws, ws_bytes = _byte_range(workspace)
+    _check(_lib.zero_norm_pieces(_addr(d_pieces), n_pieces, _addr(sq), _addr(tensor_sq),
+                                 0 if tensor_sq is None else tensor_sq.numel(), _spec(spec), ws,
+                                 ws_bytes, _stream(stream)), "zero_norm_pieces")
+
+
+def zero_scale_pieces(d_pieces: Ptr, n_pieces: int, clip: Ptr, stream=None) -> None:
+    """Every piece times clip[1], into its place."""
+    _check(_lib.zero_scale_pieces(_addr(d_pieces), n_pieces, _addr(clip), _stream(stream)),
+           "zero_scale_pieces")
+
+
+def _step_clipped(name: str, partials, state, shard_len: int, d_chunks: Ptr, n_chunks: int, consts,
+                  clip: Ptr, gdt: Optional[int], stream) -> None:
+    gdt = _gdt_of(partials) if gdt is None else gdt
+    _check(getattr(_lib, name)(_partial_array(partials), len(partials), gdt, *map(_addr, state),
+                               shard_len, _addr(d_chunks), n_chunks, *consts, _addr(clip),
+                               _stream(stream)), name)
+
+
+def zero_shard_step_clipped(partials: Sequence[Ptr], master: Ptr, m: Ptr, v: Ptr, shard_len: int,
+                            d_chunks: Ptr, n_chunks: int, hp: HParams, clip: Ptr,
+                            gdt: Optional[int] = None, stream=None) -> None:
+    """zero_shard_step on the gradient times clip[1]; from a reduced gradient
+    partials = [grad]."""
+    _step_clipped("zero_shard_step_clipped", partials, (master, m, v), shard_len, d_chunks,
+                  n_chunks, (ctypes.byref(hp),), clip, gdt, stream)
+
+
+def zero_shard_step_bf16_moments_clipped(partials: Sequence[Ptr], master: Ptr, m: Ptr, v: Ptr,
+                                         shard_len: int, d_chunks: Ptr, n_chunks: int, hp: HParams,
+                                         clip: Ptr, gdt: Optional[int] = None, stream=None) -> None:
+    """zero_shard_step_bf16_moments on the gradient times clip[1]."""
+    _step_clipped("zero_shard_step_bf16_moments_clipped", partials, (master, m, v), shard_len,
+                  d_chunks, n_chunks, (ctypes.byref(hp),), clip, gdt, stream)
+
+
+def zero_shard_step_kahan_clipped(partials: Sequence[Ptr], comp: Ptr, m: Ptr, v: Ptr,
+                                  shard_len: int, d_chunks: Ptr, n_chunks: int, hp: HParams,
+                                  clip: Ptr, gdt: Optional[int] = None, stream=None) -> None:
+    """zero_shard_step_kahan on the gradient times clip[1]."""
+    _step_clipped("zero_shard_step_kahan_clipped", partials, (comp, m, v), shard_len, d_chunks,
+                  n_chunks, (ctypes.byref(hp),), clip, gdt, stream)
+
+
+def zero_shard_step_scheduled_clipped(partials: Sequence[Ptr], master: Ptr, m: Ptr, v: Ptr,
+                                      shard_len: int, d_chunks: Ptr, n_chunks: int, consts: Ptr,
+                                      n_consts: int, index: Ptr, clip: Ptr,
+                                      gdt: Optional[int] = None, stream=None) -> None:
+    """zero_shard_step_scheduled on the gradient times clip[1]."""
+    _step_clipped("zero_shard_step_scheduled_clipped", partials, (master, m, v), shard_len,
+                  d_chunks, n_chunks, (_addr(consts), n_consts, _addr(index)), clip, gdt, stream)
+
+
+def zero_shard_step_bf16_moments_scheduled_clipped(partials: Sequence[Ptr], master: Ptr, m: Ptr,
+                                                   v: Ptr, shard_len: int, d_chunks: Ptr,
+                                                   n_chunks: int, consts: Ptr, n_consts: int,
+                                                   index: Ptr, clip: Ptr,
+                                                   gdt: Optional[int] = None, stream=None) -> None:
+    """zero_shard_step_bf16_moments_scheduled on the gradient times clip[1]."""
+    _step_clipped("zero_shard_step_bf16_moments_scheduled_clipped", partials, (master, m, v),
+                  shard_len, d_chunks, n_chunks, (_addr(consts), n_consts, _addr(index)), clip, gdt,
+                  stream)
+
+
+def zero_shard_step_kahan_scheduled_clipped(partials: Sequence[Ptr], comp: Ptr, m: Ptr, v: Ptr,
+                                            shard_len: int, d_chunks: Ptr, n_chunks: int,
+                                            consts: Ptr, n_consts: int, index: Ptr, clip: Ptr,
+                                            gdt: Optional[int] = None, stream=None) -> None:
+    """zero_shard_step_kahan_scheduled on the gradient times clip[1]."""
+    _step_clipped("zero_shard_step_kahan_scheduled_clipped", partials, (comp, m, v), shard_len,
+                  d_chunks, n_chunks, (_addr(consts), n_consts, _addr(index)), clip, gdt, stream)
 
 
 def zero_shard_step(partials: Sequence[Ptr], master: Ptr, m: Ptr, v: Ptr, shard_len: int,

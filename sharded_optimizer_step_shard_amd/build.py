@@ -41,7 +41,8 @@ def hipcc() -> str:
     return "hipcc"
 
 
-SOURCES = ("zero_kernels.hip", "zero_probes.hip", "zero_chunks.cpp", "zero_api.cpp")
+SOURCES = ("zero_kernels.hip", "zero_clip.hip", "zero_probes.hip", "zero_chunks.cpp",
+           "zero_pieces.cpp", "zero_api.cpp")
 
 
 def build(verbose: bool = True, out: str = LIB, extra=()) -> str:

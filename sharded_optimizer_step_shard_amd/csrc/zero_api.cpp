@@ -84,6 +84,37 @@ bool valid_reduce_spec(const zero_reduce_spec *rs, int n_ranks)
     return (rs->micro_batches > 1) == (rs->acc != nullptr);
 }
 
+bool valid_clip_spec(const zero_clip_spec *c)
+{
+    return c && c->out && c->max_norm >= 0.0 && isfinite(c->eps) && c->eps >= 0.0 &&
+           isfinite(c->inv_scale) && c->inv_scale > 0.0;
+}
+
+ClipArgs clip_args(const zero_clip_spec *c)
+{
+    return c ? ClipArgs{c->max_norm, c->eps, c->inv_scale, c->out} : ClipArgs{0.0, 0.0, 1.0, nullptr};
+}
+
+// A byte range a call reads or writes; one of no bytes overlaps nothing.
+struct Span {
+    const void *p;
+    int64_t bytes;
+};
+
+// Do two of the n written ranges overlap, or one of them and one of the m read?
+bool spans_alias(const Span *written, int n, const Span *read, int m)
+{
+    for (int i = 0; i < n; ++i) {
+        for (int j = i + 1; j < n; ++j)
+            if (overlaps(written[i].p, written[i].bytes, written[j].p, written[j].bytes))
+                return true;
+        for (int j = 0; j < m; ++j)
+            if (overlaps(written[i].p, written[i].bytes, read[j].p, read[j].bytes))
+                return true;
+    }
+    return false;
+}
+
 int elem_bytes(int gdt) { return gdt == ZERO_BF16 ? 2 : 4; }   // after valid_dtype
 
 // The INVALID checks of the partial list (null list, rank count, null
@@ -165,7 +196,7 @@ const char *zero_strerror(int code)
     case ZERO_ERR_UNSUPPORTED: return "unsupported gradient dtype";
     case ZERO_ERR_ALIAS: return "input overlaps an output";
     case ZERO_ERR_HIP: return "HIP launch error";
-    case ZERO_ERR_CAPACITY: return "chunk array too small";
+    case ZERO_ERR_CAPACITY: return "table or workspace too small";
     case ZERO_ERR_NOT_DEVICE: return "array range is not device memory";
     default: return "unknown error code";
     }
@@ -182,6 +213,11 @@ struct Schedule {
     const int64_t *index;
 };
 
+// Where a clipped step finds its coefficient (device, {norm, coefficient}).
+struct Clip {
+    const double *p;
+};
+
 // The three arrays a fused step updates in place (master, m, v; or comp, m,
 // v) and their element sizes in bytes.
 struct StateArrays {
@@ -196,8 +232,8 @@ struct StateArrays {
 // set when there is nothing to launch.
 static int prepare_fused(const void *const *partials, int n_ranks, int gdt, const StateArrays &st,
                          int64_t shard_len, const zero_chunk *d_chunks, int64_t n_chunks,
-                         const zero_adamw_hparams *hp, const Schedule *sched, StepArgs &a,
-                         bool *empty)
+                         const zero_adamw_hparams *hp, const Schedule *sched, const Clip *clip,
+                         StepArgs &a, bool *empty)
 {
     *empty = true;
     int rc = check_partials(partials, n_ranks, shard_len, a.parts);
@@ -210,8 +246,10 @@ static int prepare_fused(const void *const *partials, int n_ranks, int gdt, cons
     if (sched && (sched->n < 0 || sched->n > INT32_MAX ||
                   (shard_len > 0 && (!sched->consts || !sched->index || sched->n < 1))))
         return ZERO_ERR_INVALID;
+    if (clip && shard_len > 0 && !clip->p)
+        return ZERO_ERR_INVALID;
     if (!partials_aligned(a.parts, n_ranks) || !aligned16(st.p[0]) || !aligned16(st.p[1]) ||
-        !aligned16(st.p[2]) || !aligned16(d_chunks))
+        !aligned16(st.p[2]) || !aligned16(d_chunks) || (clip && !aligned16(clip->p)))
         return ZERO_ERR_MISALIGNED;
     if (sched && (!aligned16(sched->consts) || ((uintptr_t)sched->index & 7u) != 0))
         return ZERO_ERR_MISALIGNED;
@@ -233,6 +271,10 @@ static int prepare_fused(const void *const *partials, int n_ranks, int gdt, cons
             if (overlaps(sched->consts, cb, st.p[i], sb[i]) ||
                 overlaps(sched->index, 8, st.p[i], sb[i]))
                 return ZERO_ERR_ALIAS;
+    if (clip && shard_len > 0)
+        for (int i = 0; i < 3; ++i)
+            if (overlaps(clip->p, 16, st.p[i], sb[i]))
+                return ZERO_ERR_ALIAS;
     if (n_chunks == 0 || shard_len == 0)
         return ZERO_OK;
     for (int k = 0; k < n_ranks; ++k)
@@ -244,6 +286,8 @@ static int prepare_fused(const void *const *partials, int n_ranks, int gdt, cons
     if (!in_device_alloc(d_chunks, n_chunks * (int64_t)sizeof(zero_chunk)))
         return ZERO_ERR_NOT_DEVICE;
     if (sched && (!in_device_alloc(sched->consts, cb) || !in_device_alloc(sched->index, 8)))
+        return ZERO_ERR_NOT_DEVICE;
+    if (clip && !in_device_alloc(clip->p, 16))
         return ZERO_ERR_NOT_DEVICE;
     a.red = make_reduce(n_ranks);
     if (sched) {
@@ -257,6 +301,7 @@ static int prepare_fused(const void *const *partials, int n_ranks, int gdt, cons
     a.n_chunks = n_chunks;
     a.shard_len = shard_len;
     a.acc = nullptr;
+    a.clip = clip ? clip->p : nullptr;
     *empty = false;
     return ZERO_OK;
 }
@@ -265,11 +310,11 @@ static int prepare_fused(const void *const *partials, int n_ranks, int gdt, cons
 static int prepare_step(const void *const *partials, int n_ranks, int gdt, float *master,
                         float *m, float *v, int64_t shard_len, const zero_chunk *d_chunks,
                         int64_t n_chunks, const zero_adamw_hparams *hp, StepArgs &a, bool *empty,
-                        const Schedule *sched = nullptr)
+                        const Schedule *sched = nullptr, const Clip *clip = nullptr)
 {
     const StateArrays st{{master, m, v}, {4, 4, 4}};
     const int rc = prepare_fused(partials, n_ranks, gdt, st, shard_len, d_chunks, n_chunks, hp,
-                                 sched, a, empty);
+                                 sched, clip, a, empty);
     a.master = master;
     a.m = m;
     a.v = v;
@@ -282,11 +327,11 @@ static int prepare_step(const void *const *partials, int n_ranks, int gdt, float
 static int prepare_m16(const void *const *partials, int n_ranks, int gdt, float *master,
                        uint16_t *m, uint16_t *v, int64_t shard_len, const zero_chunk *d_chunks,
                        int64_t n_chunks, const zero_adamw_hparams *hp, StepArgs &a, bool *empty,
-                       const Schedule *sched = nullptr)
+                       const Schedule *sched = nullptr, const Clip *clip = nullptr)
 {
     const StateArrays st{{master, m, v}, {4, 2, 2}};
     const int rc = prepare_fused(partials, n_ranks, gdt, st, shard_len, d_chunks, n_chunks, hp,
-                                 sched, a, empty);
+                                 sched, clip, a, empty);
     a.master = master;
     a.m = (float *)m;
     a.v = (float *)v;
@@ -299,11 +344,11 @@ static int prepare_m16(const void *const *partials, int n_ranks, int gdt, float 
 static int prepare_kahan(const void *const *partials, int n_ranks, int gdt, uint16_t *comp,
                          uint16_t *m, uint16_t *v, int64_t shard_len, const zero_chunk *d_chunks,
                          int64_t n_chunks, const zero_adamw_hparams *hp, StepArgs &a, bool *empty,
-                         const Schedule *sched = nullptr)
+                         const Schedule *sched = nullptr, const Clip *clip = nullptr)
 {
     const StateArrays st{{comp, m, v}, {2, 2, 2}};
     const int rc = prepare_fused(partials, n_ranks, gdt, st, shard_len, d_chunks, n_chunks, hp,
-                                 sched, a, empty);
+                                 sched, clip, a, empty);
     a.master = nullptr;
     a.m = (float *)m;
     a.v = (float *)v;
@@ -528,6 +573,230 @@ int zero_shard_step_kahan_scheduled(const void *const *partials, int n_ranks, in
     if (rc || empty)
         return rc;
     return hip_status(launch_step_sched(a, (zero_dtype)gdt, StateLayout::Kahan, stream));
+}
+
+// The six clipped steps: check as the step each is named after, then launch.
+static int step_clipped(int rc, bool empty, const StepArgs &a, int gdt, StateLayout layout,
+                        hipStream_t stream)
+{
+    if (rc || empty)
+        return rc;
+    return hip_status(launch_step_clipped(a, (zero_dtype)gdt, layout, stream));
+}
+
+int zero_shard_step_clipped(const void *const *partials, int n_ranks, int gdt,
+                            float *master, float *m, float *v, int64_t shard_len,
+                            const zero_chunk *d_chunks, int64_t n_chunks,
+                            const zero_adamw_hparams *hp, const double *clip, hipStream_t stream)
+{
+    StepArgs a{};
+    bool empty;
+    const Clip c{clip};
+    const int rc = prepare_step(partials, n_ranks, gdt, master, m, v, shard_len, d_chunks,
+                                n_chunks, hp, a, &empty, nullptr, &c);
+    return step_clipped(rc, empty, a, gdt, StateLayout::Fp32, stream);
+}
+
+int zero_shard_step_bf16_moments_clipped(const void *const *partials, int n_ranks, int gdt,
+                                         float *master, uint16_t *m, uint16_t *v, int64_t shard_len,
+                                         const zero_chunk *d_chunks, int64_t n_chunks,
+                                         const zero_adamw_hparams *hp, const double *clip,
+                                         hipStream_t stream)
+{
+    StepArgs a{};
+    bool empty;
+    const Clip c{clip};
+    const int rc = prepare_m16(partials, n_ranks, gdt, master, m, v, shard_len, d_chunks,
+                               n_chunks, hp, a, &empty, nullptr, &c);
+    return step_clipped(rc, empty, a, gdt, StateLayout::Bf16Moments, stream);
+}
+
+int zero_shard_step_kahan_clipped(const void *const *partials, int n_ranks, int gdt,
+                                  uint16_t *comp, uint16_t *m, uint16_t *v, int64_t shard_len,
+                                  const zero_chunk *d_chunks, int64_t n_chunks,
+                                  const zero_adamw_hparams *hp, const double *clip,
+                                  hipStream_t stream)
+{
+    StepArgs a{};
+    bool empty;
+    const Clip c{clip};
+    const int rc = prepare_kahan(partials, n_ranks, gdt, comp, m, v, shard_len, d_chunks,
+                                 n_chunks, hp, a, &empty, nullptr, &c);
+    return step_clipped(rc, empty, a, gdt, StateLayout::Kahan, stream);
+}
+
+int zero_shard_step_scheduled_clipped(const void *const *partials, int n_ranks, int gdt,
+                                      float *master, float *m, float *v, int64_t shard_len,
+                                      const zero_chunk *d_chunks, int64_t n_chunks,
+                                      const zero_step_consts *consts, int64_t n_consts,
+                                      const int64_t *index, const double *clip, hipStream_t stream)
+{
+    StepArgs a{};
+    bool empty;
+    const Schedule sched{consts, n_consts, index};
+    const Clip c{clip};
+    const int rc = prepare_step(partials, n_ranks, gdt, master, m, v, shard_len, d_chunks,
+                                n_chunks, nullptr, a, &empty, &sched, &c);
+    return step_clipped(rc, empty, a, gdt, StateLayout::Fp32, stream);
+}
+
+int zero_shard_step_bf16_moments_scheduled_clipped(const void *const *partials, int n_ranks, int gdt,
+                                                   float *master, uint16_t *m, uint16_t *v,
+                                                   int64_t shard_len, const zero_chunk *d_chunks,
+                                                   int64_t n_chunks, const zero_step_consts *consts,
+                                                   int64_t n_consts, const int64_t *index,
+                                                   const double *clip, hipStream_t stream)
+{
+    StepArgs a{};
+    bool empty;
+    const Schedule sched{consts, n_consts, index};
+    const Clip c{clip};
+    const int rc = prepare_m16(partials, n_ranks, gdt, master, m, v, shard_len, d_chunks,
+                               n_chunks, nullptr, a, &empty, &sched, &c);
+    return step_clipped(rc, empty, a, gdt, StateLayout::Bf16Moments, stream);
+}
+
+int zero_shard_step_kahan_scheduled_clipped(const void *const *partials, int n_ranks, int gdt,
+                                            uint16_t *comp, uint16_t *m, uint16_t *v,
+                                            int64_t shard_len, const zero_chunk *d_chunks,
+                                            int64_t n_chunks, const zero_step_consts *consts,
+                                            int64_t n_consts, const int64_t *index,
+                                            const double *clip, hipStream_t stream)
+{
+    StepArgs a{};
+    bool empty;
+    const Schedule sched{consts, n_consts, index};
+    const Clip c{clip};
+    const int rc = prepare_kahan(partials, n_ranks, gdt, comp, m, v, shard_len, d_chunks,
+                                 n_chunks, nullptr, a, &empty, &sched, &c);
+    return step_clipped(rc, empty, a, gdt, StateLayout::Kahan, stream);
+}
+
+int64_t zero_norm_workspace(int64_t n_pieces)
+{
+    if (n_pieces < 0 || n_pieces > INT32_MAX)
+        return -1;
+    return 8 * (n_pieces < ZERO_NORM_PARTIALS ? (int64_t)ZERO_NORM_PARTIALS : n_pieces);
+}
+
+int zero_reduce_norm_shard(const void *const *partials, int n_ranks, int gdt,
+                           const zero_reduce_spec *rs, int64_t n, float *grad_out, double *sq,
+                           const zero_clip_spec *spec, void *workspace, int64_t workspace_bytes,
+                           hipStream_t stream)
+{
+    const zero_reduce_spec flat = {0, 1, nullptr};
+    const zero_reduce_spec *r = rs ? rs : &flat;
+    ReduceNormArgs a;
+    int rc = check_partials(partials, n_ranks, n, a.parts);
+    if (rc)
+        return rc;
+    if (bad_len(n) || !sq || !workspace || workspace_bytes < 0 || (spec && !valid_clip_spec(spec)) ||
+        !valid_reduce_spec(r, n_ranks))
+        return ZERO_ERR_INVALID;
+    const int64_t need = zero_norm_workspace(0);
+    if (workspace_bytes < need)
+        return ZERO_ERR_CAPACITY;
+    if (!partials_aligned(a.parts, n_ranks) || !aligned16(grad_out) || !aligned16(r->acc) ||
+        !aligned16(workspace) || ((uintptr_t)sq & 7u) != 0 || (spec && !aligned16(spec->out)))
+        return ZERO_ERR_MISALIGNED;
+    if (!valid_dtype(gdt))
+        return ZERO_ERR_UNSUPPORTED;
+    const int64_t gb = n * elem_bytes(gdt);
+    Span read[ZERO_MAX_RANKS + 1];
+    for (int k = 0; k < n_ranks; ++k)
+        read[k] = {partials[k], gb};
+    // grad_out may be the accumulator itself: each element is read, then
+    // written, by the same lane
+    read[n_ranks] = {r->acc, r->acc && r->acc != grad_out ? n * 4 : 0};
+    const Span written[4] = {{grad_out, grad_out ? n * 4 : 0}, {sq, 8},
+                             {spec ? spec->out : nullptr, spec ? 16 : 0}, {workspace, need}};
+    if (spans_alias(written, 4, read, n_ranks + 1))
+        return ZERO_ERR_ALIAS;
+    for (int k = 0; k < n_ranks; ++k)
+        if (!in_device_alloc(partials[k], gb))
+            return ZERO_ERR_NOT_DEVICE;
+    for (const Span &w : written)
+        if (!in_device_alloc(w.p, w.bytes))
+            return ZERO_ERR_NOT_DEVICE;
+    if (r->acc && !in_device_alloc(r->acc, n * 4))
+        return ZERO_ERR_NOT_DEVICE;
+    a.red = make_reduce(n_ranks, r->group, r->micro_batches);
+    a.acc = r->acc;
+    a.out = grad_out;
+    a.part = (double *)workspace;
+    a.n = n;
+    FinishArgs f{};
+    f.sq = sq;
+    f.clip = clip_args(spec);
+    return hip_status(launch_reduce_norm(a, (zero_dtype)gdt, f, stream));
+}
+
+int zero_clip_coef(const double *sq, int64_t n_sq, const zero_clip_spec *spec, hipStream_t stream)
+{
+    if (!sq || n_sq < 1 || n_sq > INT32_MAX || !valid_clip_spec(spec))
+        return ZERO_ERR_INVALID;
+    if (((uintptr_t)sq & 7u) != 0 || !aligned16(spec->out))
+        return ZERO_ERR_MISALIGNED;
+    if (overlaps(sq, n_sq * 8, spec->out, 16))
+        return ZERO_ERR_ALIAS;
+    if (!in_device_alloc(sq, n_sq * 8) || !in_device_alloc(spec->out, 16))
+        return ZERO_ERR_NOT_DEVICE;
+    return hip_status(launch_clip_coef(sq, n_sq, clip_args(spec), stream));
+}
+
+int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, double *tensor_sq,
+                     int64_t n_tensors, const zero_clip_spec *spec, void *workspace,
+                     int64_t workspace_bytes, hipStream_t stream)
+{
+    if (n_pieces < 0 || n_pieces > INT32_MAX || (n_pieces > 0 && !d_pieces) || n_tensors < 0 ||
+        n_tensors > INT32_MAX || !sq || !workspace || workspace_bytes < 0 ||
+        (spec && !valid_clip_spec(spec)))
+        return ZERO_ERR_INVALID;
+    const int64_t need = zero_norm_workspace(n_pieces);
+    if (workspace_bytes < need)
+        return ZERO_ERR_CAPACITY;
+    if (!aligned16(d_pieces) || !aligned16(workspace) || ((uintptr_t)sq & 7u) != 0 ||
+        ((uintptr_t)tensor_sq & 7u) != 0 || (spec && !aligned16(spec->out)))
+        return ZERO_ERR_MISALIGNED;
+    const Span read[1] = {{d_pieces, n_pieces * (int64_t)sizeof(zero_piece)}};
+    const Span written[4] = {{sq, 8}, {tensor_sq, tensor_sq ? n_tensors * 8 : 0},
+                             {spec ? spec->out : nullptr, spec ? 16 : 0}, {workspace, need}};
+    if (spans_alias(written, 4, read, 1))
+        return ZERO_ERR_ALIAS;
+    if (!in_device_alloc(read[0].p, read[0].bytes))
+        return ZERO_ERR_NOT_DEVICE;
+    for (const Span &w : written)
+        if (!in_device_alloc(w.p, w.bytes))
+            return ZERO_ERR_NOT_DEVICE;
+    PiecesArgs a{};
+    a.pieces = d_pieces;
+    a.n_pieces = n_pieces;
+    a.part = (double *)workspace;
+    FinishArgs f{};
+    f.sq = sq;
+    f.clip = clip_args(spec);
+    f.tensor_sq = n_tensors > 0 ? tensor_sq : nullptr;
+    f.n_tensors = n_tensors;
+    return hip_status(launch_norm_pieces(a, f, stream));
+}
+
+int zero_scale_pieces(const zero_piece *d_pieces, int64_t n_pieces, const double *clip,
+                      hipStream_t stream)
+{
+    if (n_pieces < 0 || n_pieces > INT32_MAX || (n_pieces > 0 && !d_pieces) || !clip)
+        return ZERO_ERR_INVALID;
+    if (!aligned16(d_pieces) || !aligned16(clip))
+        return ZERO_ERR_MISALIGNED;
+    if (n_pieces == 0)
+        return ZERO_OK;
+    if (!in_device_alloc(d_pieces, n_pieces * (int64_t)sizeof(zero_piece)) ||
+        !in_device_alloc(clip, 16))
+        return ZERO_ERR_NOT_DEVICE;
+    PiecesArgs a{};
+    a.pieces = d_pieces;
+    a.n_pieces = n_pieces;
+    a.clip = clip;
+    return hip_status(launch_scale_pieces(a, stream));
 }
 
 int zero_accumulate_shard(const void *const *partials, int n_ranks, int gdt, int group,

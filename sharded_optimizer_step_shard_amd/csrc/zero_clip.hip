@@ -1,0 +1,582 @@
+// Clipping by the global gradient norm: the reduce with its sum of squares,
+// sums of squares of many tensors, the coefficient, many tensors times the
+// coefficient, and the clipped steps.
+//
+// All of it is streams: two operations an element for a sum of squares, one
+// for a scaling, so the bound is HBM bandwidth and every load and store is 16
+// bytes a lane.  A square is exact in double (an fp32 value has 24 bits), and
+// the sums are kept in double: they can neither overflow nor lose small terms
+// before some 2^29 equal ones, and the double pipe has room beside the stream.
+//
+// Sums without atomics: each workgroup (one wave) leaves one double, and one
+// workgroup of a second launch adds those in a fixed order.  The order depends
+// on the element count or the table alone, so results repeat bit for bit.
+
+#include "zero_device.h"
+
+namespace zs {
+
+namespace {
+
+constexpr int kFinishBlock = 1024;
+constexpr int kFinishWaves = kFinishBlock / kStepLanes;
+
+// The sum over the 64 lanes, in every lane: pairs, then pairs of pairs.
+__device__ __forceinline__ double wave_sum(double x)
+{
+#pragma unroll
+    for (int d = 1; d < kStepLanes; d *= 2)
+        x = x + __shfl_xor(x, d);
+    return x;
+}
+
+__device__ __forceinline__ double square_add(double x, double s) { return __builtin_fma(x, x, s); }
+
+// norm and coefficient (zero_clip_coef in the header).  A sum that is not
+// finite (it has an infinity or a NaN in it: finite fp32 squares cannot
+// overflow a double's sum) makes the coefficient NaN.
+__device__ __forceinline__ void write_clip(double sq, const ClipArgs &c)
+{
+    const double norm = c.inv_scale * __builtin_sqrt(sq);
+    const double d = norm + c.eps;
+    double coef = d <= c.max_norm ? c.inv_scale : c.inv_scale * (c.max_norm / d);
+    if (!(sq < __builtin_inf()))
+        coef = __builtin_nan("");
+    c.out[0] = norm;
+    c.out[1] = coef;
+}
+
+// ------------------------------------------------------- finishing the sums
+
+// The sum of part[0 .. n) by a whole workgroup of kFinishBlock lanes: lane i
+// adds part[i], part[i + kFinishBlock], ..., then the waves' sums are added in
+// order.  Returned in wave 0.
+__device__ __forceinline__ double block_sum(const double *part, int64_t n)
+{
+    __shared__ double waves[kFinishWaves];
+    double s = 0.0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += kFinishBlock)
+        s = s + part[i];
+    s = wave_sum(s);
+    if (threadIdx.x % kStepLanes == 0)
+        waves[threadIdx.x / kStepLanes] = s;
+    __syncthreads();
+    double t = waves[0];
+#pragma unroll
+    for (int w = 1; w < kFinishWaves; ++w)
+        t = t + waves[w];
+    return t;
+}
+
+// Tensor sums: the wave that meets a tensor's first piece adds its pieces.
+__device__ __forceinline__ void tensor_sums(const FinishArgs &a, int64_t wave, int64_t n_waves)
+{
+    const int lane = threadIdx.x % kStepLanes;
+    for (int64_t p = wave; p < a.n_part; p += n_waves) {
+        int64_t count = a.pieces[p].tensor_pieces;
+        const int64_t id = a.pieces[p].tensor_id;
+        if (count <= 0 || id < 0 || id >= a.n_tensors)
+            continue;
+        if (count > a.n_part - p)
+            count = a.n_part - p;
+        double s = 0.0;
+        for (int64_t i = lane; i < count; i += kStepLanes)
+            s = s + a.part[p + i];
+        s = wave_sum(s);
+        if (lane == 0)
+            a.tensor_sq[id] = s;
+    }
+}
+
+// Workgroup 0 makes the total and the coefficient; the others, launched where
+// they are asked for, the tensors' sums.
+__global__ __launch_bounds__(kFinishBlock) void norm_finish_kernel(FinishArgs a)
+{
+    if (blockIdx.x > 0) {
+        tensor_sums(a, (int64_t)(blockIdx.x - 1) * kFinishWaves + threadIdx.x / kStepLanes,
+                    (int64_t)(gridDim.x - 1) * kFinishWaves);
+        return;
+    }
+    const double s = block_sum(a.part, a.n_part);
+    if (threadIdx.x == 0) {
+        a.sq[0] = s;
+        if (a.clip.out)
+            write_clip(s, a.clip);
+    }
+}
+
+__global__ __launch_bounds__(kStepLanes) void clip_coef_kernel(const double *sq, int64_t n, ClipArgs c)
+{
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += kStepLanes)
+        s = s + sq[i];
+    s = wave_sum(s);
+    if (threadIdx.x == 0)
+        write_clip(s, c);
+}
+
+// ------------------------------------------------------- reduce with the norm
+
+// The launch of the accumulate kernel: one wave a workgroup, workgroup b on
+// spans b, b + gridDim.x, ... of kNormSpan elements, and its squares in one
+// double of each lane until the end.
+constexpr int64_t kNormSpan = 2048;
+
+// DIV: 1 multiplies by the exact reciprocal of a power of two, 2 divides.
+template <zero_dtype G, int NC, int KC, int DIV>
+__device__ __forceinline__ double reduce_norm_spans(const ReduceNormArgs &a)
+{
+    constexpr int VEC = Grad<G>::VEC;
+    constexpr int64_t GPS = kNormSpan / VEC;
+    const int n = NC > 0 ? NC : a.red.n_ranks;
+    const int64_t groups = a.n / VEC;
+    double sq = 0.0;
+    for (int64_t sp = blockIdx.x; sp * GPS < groups; sp += gridDim.x) {
+        const int64_t gend = (sp + 1) * GPS < groups ? (sp + 1) * GPS : groups;
+        for (int64_t g = sp * GPS + threadIdx.x; g < gend; g += kStepBlock) {
+            const int64_t i0 = g * VEC;
+            F32x<VEC> acc, out;
+            if (a.acc)
+                acc.load(a.acc + i0);
+            double s[VEC];
+            if constexpr (KC < 0)
+                group_sum<G, NC, kStepBatch>(s, a.parts, n, i0);
+            else
+                group_sum_two_level<G, NC, KC, kStepBatch>(s, a.parts, n, a.red.group, i0);
+            if (a.acc) {
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    s[j] = (double)acc[j] + s[j];
+            }
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                out[j] = DIV == 1 ? (float)(s[j] * a.red.inv_n) : (float)(s[j] / a.red.n);
+                sq = square_add((double)out[j], sq);
+            }
+            if (a.out)
+                out.store(a.out + i0);
+        }
+    }
+    if (blockIdx.x == 0) {
+        const int64_t i = groups * VEC + threadIdx.x;   // the last n % VEC elements
+        if (i < a.n) {
+            double e = elem_sum_two_level<G>(a.parts, n, a.red.group, i);
+            if (a.acc)
+                e = (double)a.acc[i] + e;
+            const float f = finish_reduce<0>(e, a.red);
+            sq = square_add((double)f, sq);
+            if (a.out)
+                a.out[i] = f;
+        }
+    }
+    return sq;
+}
+
+template <zero_dtype G, int NC, int KC>
+__global__ __launch_bounds__(kStepBlock) __attribute__((amdgpu_waves_per_eu(1, 1)))
+void reduce_norm_kernel(ReduceNormArgs a)
+{
+    const double sq = wave_sum(a.red.pow2 ? reduce_norm_spans<G, NC, KC, 1>(a)
+                                          : reduce_norm_spans<G, NC, KC, 2>(a));
+    if (threadIdx.x == 0)
+        a.part[blockIdx.x] = sq;
+}
+
+// ------------------------------------------------------- many tensors
+
+// A piece starts at any multiple of its element size: 16-byte loads and
+// stores at such an address, which gfx950 does in one access.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+__device__ __forceinline__ u32x4 ld_any(const void *p)
+{
+    return __builtin_nontemporal_load((const u32x4_any *)p);
+}
+
+__device__ __forceinline__ double half_to_double(uint32_t h)
+{
+    return (double)(float)__builtin_bit_cast(_Float16, (uint16_t)h);
+}
+
+// VEC elements of one 16-byte word, widened.
+template <int DT> struct Elem;
+
+template <> struct Elem<ZERO_FP32> {
+    static constexpr int VEC = 4, BYTES = 4;
+    __device__ static __forceinline__ void widen(double *x, u32x4 r) { Grad<ZERO_FP32>::first(x, r); }
+    __device__ static __forceinline__ double one(const void *p, int64_t i) { return (double)((const float *)p)[i]; }
+    __device__ static __forceinline__ void put(void *p, int64_t i, double y) { ((float *)p)[i] = (float)y; }
+};
+
+template <> struct Elem<ZERO_BF16> {
+    static constexpr int VEC = 8, BYTES = 2;
+    __device__ static __forceinline__ void widen(double *x, u32x4 r) { Grad<ZERO_BF16>::first(x, r); }
+    __device__ static __forceinline__ double one(const void *p, int64_t i)
+    {
+        return bf16_to_double(((const uint16_t *)p)[i]);
+    }
+    __device__ static __forceinline__ uint32_t narrow(double y) { return bf16_from_double(y); }
+    __device__ static __forceinline__ void put(void *p, int64_t i, double y) { ((uint16_t *)p)[i] = (uint16_t)narrow(y); }
+};
+
+template <> struct Elem<ZERO_FP16> {
+    static constexpr int VEC = 8, BYTES = 2;
+    __device__ static __forceinline__ void widen(double *x, u32x4 r)
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            x[2 * q] = half_to_double(r[q] & 0xFFFFu);
+            x[2 * q + 1] = half_to_double(r[q] >> 16);
+        }
+    }
+    __device__ static __forceinline__ double one(const void *p, int64_t i)
+    {
+        return half_to_double(((const uint16_t *)p)[i]);
+    }
+    // double -> fp16 in one rounding, by way of fp32 rounded to odd, as
+    // bf16_from_double (fp32 keeps 13 more bits than fp16, subnormals included)
+    __device__ static __forceinline__ uint32_t narrow(double y)
+    {
+        const float f = (float)y;
+        const double fd = (double)f;
+        uint32_t u = __float_as_uint(f);
+        if (__builtin_fabs(fd) > __builtin_fabs(y))
+            u -= 1;
+        if (fd != y)
+            u |= 1;
+        return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)__uint_as_float(u));
+    }
+    __device__ static __forceinline__ void put(void *p, int64_t i, double y) { ((uint16_t *)p)[i] = (uint16_t)narrow(y); }
+};
+
+// The descriptor of piece pi, with scalar loads (as chunk_at); a malformed one
+// comes back empty.
+__device__ __forceinline__ zero_piece piece_at(const zero_piece *table, int64_t pi)
+{
+    const char *p = (const char *)(table + __builtin_amdgcn_readfirstlane((int)pi));
+    zero_piece c;
+    c.src = (const void *)(uintptr_t)*(const_i64 *)(p + offsetof(zero_piece, src));
+    c.dst = (void *)(uintptr_t)*(const_i64 *)(p + offsetof(zero_piece, dst));
+    c.len = *(const_i32 *)(p + offsetof(zero_piece, len));
+    const uint32_t dts = (uint32_t)*(const_i32 *)(p + offsetof(zero_piece, src_dt));
+    c.src_dt = (int16_t)(dts & 0xFFFFu);
+    c.dst_dt = (int16_t)(dts >> 16);
+    c.tensor_id = 0;
+    c.tensor_pieces = 0;
+    if (c.len < 0 || c.len > (1 << 24) || !c.src)
+        c.len = 0;
+    return c;
+}
+
+// This lane's part of a piece's sum of squares: kPieceUnroll loads of 16
+// bytes in flight, lanes past the end adding zeros.
+constexpr int kPieceUnroll = 8;
+
+template <int DT>
+__device__ __forceinline__ double piece_square(const zero_piece &c)
+{
+    using E = Elem<DT>;
+    const char *src = (const char *)c.src;
+    const int words = c.len / E::VEC;
+    double s[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int w0 = 0; w0 < words; w0 += kPieceUnroll * kStepLanes) {
+        u32x4 r[kPieceUnroll];
+#pragma unroll
+        for (int u = 0; u < kPieceUnroll; ++u) {
+            const int w = w0 + u * kStepLanes + (int)threadIdx.x % kStepLanes;
+            r[u] = w < words ? ld_any(src + (int64_t)w * 16) : (u32x4){0u, 0u, 0u, 0u};
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < kPieceUnroll; ++u) {
+            double x[E::VEC];
+            E::widen(x, r[u]);
+#pragma unroll
+            for (int j = 0; j < E::VEC; ++j)
+                s[j % 4] = square_add(x[j], s[j % 4]);
+        }
+    }
+    const int i = words * E::VEC + (int)threadIdx.x % kStepLanes;
+    if (i < c.len)
+        s[0] = square_add(E::one(c.src, i), s[0]);
+    return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __forceinline__ double piece_sum(const zero_piece &c)
+{
+    double s = 0.0;
+    if (c.src_dt == ZERO_BF16)
+        s = piece_square<ZERO_BF16>(c);
+    else if (c.src_dt == ZERO_FP32)
+        s = piece_square<ZERO_FP32>(c);
+    else if (c.src_dt == ZERO_FP16)
+        s = piece_square<ZERO_FP16>(c);
+    return wave_sum(s);
+}
+
+__global__ __launch_bounds__(kStepBlock) void norm_pieces_kernel(PiecesArgs a)
+{
+    for (int64_t p = blockIdx.x; p < a.n_pieces; p += gridDim.x) {
+        const double s = piece_sum(piece_at(a.pieces, p));
+        if (threadIdx.x == 0)
+            a.part[p] = s;
+    }
+}
+
+// coef times a piece.  The stores are aligned: up to 15 bytes before dst's
+// first 16-byte boundary are done element by element, as is the end; the loads
+// go by them, at any address.
+template <int S, int D>
+__device__ __forceinline__ void scale_piece(const zero_piece &c, double coef)
+{
+    using ES = Elem<S>;
+    using ED = Elem<D>;
+    constexpr int VEC = 8;
+    constexpr int NS = VEC / ES::VEC, ND = VEC / ED::VEC;   // 16-byte words of a group
+    const int lane = (int)threadIdx.x % kStepLanes;
+    int head = (int)((16u - ((uintptr_t)c.dst & 15u)) & 15u) / ED::BYTES;
+    if (head > c.len)
+        head = c.len;
+    const int groups = (c.len - head) / VEC;
+    const int tail = head + groups * VEC;
+    const char *src = (const char *)c.src + (int64_t)head * ES::BYTES;
+    char *dst = (char *)c.dst + (int64_t)head * ED::BYTES;
+    if (lane < head)
+        ED::put(c.dst, lane, coef * ES::one(c.src, lane));
+    if (tail + lane < c.len)
+        ED::put(c.dst, tail + lane, coef * ES::one(c.src, tail + lane));
+    constexpr int U = 8 / NS;
+    for (int g0 = 0; g0 < groups; g0 += U * kStepLanes) {
+        u32x4 r[U][NS];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + u * kStepLanes + lane;
+            if (g < groups) {
+#pragma unroll
+                for (int q = 0; q < NS; ++q)
+                    r[u][q] = ld_any(src + ((int64_t)g * NS + q) * 16);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int g = g0 + u * kStepLanes + lane;
+            if (g >= groups)
+                break;
+            double x[VEC];
+#pragma unroll
+            for (int q = 0; q < NS; ++q)
+                ES::widen(x + q * ES::VEC, r[u][q]);
+#pragma unroll
+            for (int q = 0; q < ND; ++q) {
+                u32x4 o;
+                if constexpr (D == ZERO_FP32) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = __float_as_uint((float)(coef * x[4 * q + j]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        o[j] = ED::narrow(coef * x[2 * j]) | (ED::narrow(coef * x[2 * j + 1]) << 16);
+                }
+                st_nt((u32x4 *)(dst + ((int64_t)g * ND + q) * 16), o);
+            }
+        }
+    }
+}
+
+template <int S>
+__device__ __forceinline__ void scale_to(const zero_piece &c, double coef)
+{
+    if (c.dst_dt == ZERO_BF16)
+        scale_piece<S, ZERO_BF16>(c, coef);
+    else if (c.dst_dt == ZERO_FP32)
+        scale_piece<S, ZERO_FP32>(c, coef);
+    else if (c.dst_dt == ZERO_FP16)
+        scale_piece<S, ZERO_FP16>(c, coef);
+}
+
+__global__ __launch_bounds__(kStepBlock) void scale_pieces_kernel(PiecesArgs a)
+{
+    const double coef = ((const const_f64 *)a.clip)[1];
+    if (!(coef == coef))
+        return;
+    for (int64_t p = blockIdx.x; p < a.n_pieces; p += gridDim.x) {
+        const zero_piece c = piece_at(a.pieces, p);
+        if (c.len == 0 || !c.dst || (coef == 1.0 && c.dst == c.src && c.dst_dt == c.src_dt))
+            continue;
+        if (c.src_dt == ZERO_BF16)
+            scale_to<ZERO_BF16>(c, coef);
+        else if (c.src_dt == ZERO_FP32)
+            scale_to<ZERO_FP32>(c, coef);
+        else if (c.src_dt == ZERO_FP16)
+            scale_to<ZERO_FP16>(c, coef);
+    }
+}
+
+// ------------------------------------------------------- the clipped steps
+
+// Resident waves per SIMD, as the steps that do not clip.
+template <int L, zero_dtype G, int NC, bool SMALL>
+constexpr int kClipWaves = L == 0 ? (SMALL ? 2 : 1)
+                                  : (L == 1 ? kM16Waves<G, NC, SMALL> : kKahanWaves);
+
+// L, SMALL: as the scheduled steps.  The coefficient and, for a scheduled
+// step, the constants are read when the kernel runs.
+template <int L, zero_dtype G, int NC, bool SMALL>
+__global__ __launch_bounds__(kStepBlock) __attribute__((amdgpu_waves_per_eu(1, kClipWaves<L, G, NC, SMALL>)))
+void shard_step_clip_kernel(StepArgs a)
+{
+    const double coef = ((const const_f64 *)a.clip)[1];
+    if (!(coef == coef))
+        return;
+    StepScalars k = a.k;
+    if (a.sched) {
+        const int64_t t = *(const_i64 *)a.sched_index;
+        if (t < 0 || t >= a.n_sched)
+            return;
+        const const_f64 *e = (const const_f64 *)(a.sched + t);
+        k.b1 = e[0]; k.c1 = e[1]; k.b2 = e[2]; k.c2 = e[3]; k.bc1 = e[4]; k.bc2 = e[5];
+        k.eps = e[6]; k.lr = e[7]; k.dec = e[8]; k.wd = e[9];
+    }
+    for (int64_t ci = blockIdx.x; ci < a.n_chunks; ci += gridDim.x) {
+        if constexpr (L == 0)
+            step_chunk<G, NC, false, -1, 0, true>(a, chunk_at(a.chunks, ci), k, coef);
+        else if constexpr (L == 1)
+            step_chunk_m16<G, NC, SMALL, true>(a, chunk_at(a.chunks, ci), k, coef);
+        else
+            step_chunk_kahan<G, NC, true>(a, chunk_at(a.chunks, ci), k, coef);
+    }
+}
+
+// ------------------------------------------------------- launchers
+
+hipError_t finish(const FinishArgs &f, hipStream_t s)
+{
+    unsigned grid = 1;
+    if (f.tensor_sq && f.n_part > 0) {
+        const int64_t want = (f.n_part + kFinishWaves - 1) / kFinishWaves;
+        grid += (unsigned)(want < 1024 ? want : 1024);
+    }
+    hipLaunchKernelGGL(norm_finish_kernel, dim3(grid), dim3(kFinishBlock), 0, s, f);
+    return hipGetLastError();
+}
+
+template <zero_dtype G, int NC>
+void launch_reduce_norm_n(const ReduceNormArgs &a, int K, dim3 grid, hipStream_t s)
+{
+    const dim3 block(kStepBlock);
+    constexpr int K8 = (NC % 8 == 0 && NC > 8) ? 8 : 0;
+    constexpr int K4 = (NC % 4 == 0 && NC > 4) ? 4 : 0;
+    if (K == 1 || K == a.red.n_ranks)
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, -1>), grid, block, 0, s, a);
+    else if (K8 == 8 && K == 8)
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, K8>), grid, block, 0, s, a);
+    else if (K4 == 4 && K == 4)
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, K4>), grid, block, 0, s, a);
+    else
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, 0>), grid, block, 0, s, a);
+}
+
+template <zero_dtype G>
+hipError_t reduce_norm_dispatch(const ReduceNormArgs &a, dim3 grid, hipStream_t s)
+{
+    const int K = a.red.group;
+    switch (a.red.n_ranks) {
+    case 1: launch_reduce_norm_n<G, 1>(a, K, grid, s); break;
+    case 2: launch_reduce_norm_n<G, 2>(a, K, grid, s); break;
+    case 4: launch_reduce_norm_n<G, 4>(a, K, grid, s); break;
+    case 8: launch_reduce_norm_n<G, 8>(a, K, grid, s); break;
+    case 16: launch_reduce_norm_n<G, 16>(a, K, grid, s); break;
+    case 32: launch_reduce_norm_n<G, 32>(a, K, grid, s); break;
+    case 64: launch_reduce_norm_n<G, 64>(a, K, grid, s); break;
+    default: launch_reduce_norm_n<G, 0>(a, K, grid, s); break;
+    }
+    return hipGetLastError();
+}
+
+template <int L, zero_dtype G, bool SMALL>
+hipError_t step_clip_dispatch(const StepArgs &a, hipStream_t s)
+{
+    const dim3 grid(chunk_grid(a.n_chunks)), block(kStepBlock);
+    switch (a.red.n_ranks) {
+    case 1: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 1, SMALL>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 2, SMALL>), grid, block, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 4, SMALL>), grid, block, 0, s, a); break;
+    case 8: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 8, SMALL>), grid, block, 0, s, a); break;
+    case 16: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 16, SMALL>), grid, block, 0, s, a); break;
+    case 32: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 32, SMALL>), grid, block, 0, s, a); break;
+    case 64: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 64, SMALL>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 0, SMALL>), grid, block, 0, s, a); break;
+    }
+    return hipGetLastError();
+}
+
+template <int L>
+hipError_t step_clip_layout(const StepArgs &a, zero_dtype gdt, hipStream_t s)
+{
+    const bool small = a.n_chunks <= (L == 1 ? ZERO_SMALL_LAUNCH_CHUNKS_12B : ZERO_SMALL_LAUNCH_CHUNKS);
+    if (gdt == ZERO_BF16)
+        return small ? step_clip_dispatch<L, ZERO_BF16, true>(a, s)
+                     : step_clip_dispatch<L, ZERO_BF16, false>(a, s);
+    return small ? step_clip_dispatch<L, ZERO_FP32, true>(a, s)
+                 : step_clip_dispatch<L, ZERO_FP32, false>(a, s);
+}
+
+}  // namespace
+
+hipError_t launch_reduce_norm(const ReduceNormArgs &a, zero_dtype gdt, FinishArgs f, hipStream_t s)
+{
+    f.part = a.part;
+    f.n_part = 0;
+    if (a.n > 0) {
+        f.n_part = (a.n + kNormSpan - 1) / kNormSpan;
+        if (f.n_part > ZERO_NORM_PARTIALS)
+            f.n_part = ZERO_NORM_PARTIALS;
+        const dim3 grid((unsigned)f.n_part);
+        const hipError_t e = gdt == ZERO_BF16 ? reduce_norm_dispatch<ZERO_BF16>(a, grid, s)
+                                              : reduce_norm_dispatch<ZERO_FP32>(a, grid, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    return finish(f, s);
+}
+
+hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s)
+{
+    hipLaunchKernelGGL(clip_coef_kernel, dim3(1), dim3(kStepLanes), 0, s, sq, n, c);
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s)
+{
+    f.part = a.part;
+    f.n_part = a.n_pieces;
+    f.pieces = a.pieces;
+    if (a.n_pieces > 0) {
+        hipLaunchKernelGGL(norm_pieces_kernel, dim3(chunk_grid(a.n_pieces)), dim3(kStepBlock), 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return finish(f, s);
+}
+
+hipError_t launch_scale_pieces(const PiecesArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL(scale_pieces_kernel, dim3(chunk_grid(a.n_pieces)), dim3(kStepBlock), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_step_clipped(const StepArgs &a, zero_dtype gdt, StateLayout layout, hipStream_t s)
+{
+    switch (layout) {
+    case StateLayout::Fp32: return step_clip_layout<0>(a, gdt, s);
+    case StateLayout::Bf16Moments: return step_clip_layout<1>(a, gdt, s);
+    case StateLayout::Kahan: return step_clip_layout<2>(a, gdt, s);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace zs

@@ -53,6 +53,42 @@ struct StepArgs {
     const zero_step_consts *sched;   // scheduled step: constants table, its
     const int64_t *sched_index;      // entry index and entry count
     int64_t n_sched;
+    const double *clip;   // clipped step: {norm, coefficient}
+};
+
+// zero_clip_spec as the kernels take it; out null: no coefficient is formed.
+struct ClipArgs {
+    double max_norm, eps, inv_scale;
+    double *out;
+};
+
+// The reduce with the norm: each workgroup leaves its sum of squares in part.
+struct ReduceNormArgs {
+    PartialPtrs parts;
+    ReduceScalars red;
+    const float *acc;   // earlier micro-batches' sum, or null
+    float *out;         // reduced gradient, or null
+    double *part;
+    int64_t n;
+};
+
+// What becomes of n_part partial sums: the total, the coefficient, and, with
+// pieces given, each tensor's sum.
+struct FinishArgs {
+    const double *part;
+    int64_t n_part;
+    double *sq;
+    ClipArgs clip;
+    const zero_piece *pieces;
+    double *tensor_sq;
+    int64_t n_tensors;
+};
+
+struct PiecesArgs {
+    const zero_piece *pieces;
+    int64_t n_pieces;
+    double *part;        // norm: one sum a piece
+    const double *clip;  // scale
 };
 
 struct ReduceArgs {
@@ -97,6 +133,11 @@ hipError_t launch_accumulate(const AccArgs &a, zero_dtype gdt, hipStream_t s);
 hipError_t launch_reduce(const ReduceArgs &a, zero_dtype gdt, hipStream_t s);
 hipError_t launch_adamw(const AdamArgs &a, hipStream_t s);
 hipError_t launch_gather(const GatherArgs &a, hipStream_t s);
+hipError_t launch_step_clipped(const StepArgs &a, zero_dtype gdt, StateLayout layout, hipStream_t s);
+hipError_t launch_reduce_norm(const ReduceNormArgs &a, zero_dtype gdt, FinishArgs f, hipStream_t s);
+hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s);
+hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s);
+hipError_t launch_scale_pieces(const PiecesArgs &a, hipStream_t s);
 hipError_t launch_probe_copy(const void *src, void *dst, int64_t bytes, hipStream_t s);
 hipError_t launch_probe_read(const void *src, int64_t bytes, uint32_t *sink, uint32_t magic,
                              hipStream_t s);

@@ -1,0 +1,268 @@
+"""Clipping by the global norm, on the CPU: every refusal of its entry points
+(nothing is launched; the addresses are never dereferenced), the table of
+pieces, and the binding's own checks."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import sharded_optimizer_step_shard_amd as zs
+
+BASE = 0x7F0000000000
+INVALID, MISALIGNED, UNSUPPORTED = zs.ZERO_ERR_INVALID, zs.ZERO_ERR_MISALIGNED, zs.ZERO_ERR_UNSUPPORTED
+ALIAS, CAPACITY, NOT_DEVICE = zs.ZERO_ERR_ALIAS, zs.ZERO_ERR_CAPACITY, zs.ZERO_ERR_NOT_DEVICE
+INF, NAN = float("inf"), float("nan")
+
+
+def at(k):
+    """A range of its own for each k, far from the others."""
+    return BASE + (k << 32)
+
+
+def parts(n):
+    return (ctypes.c_void_p * max(n, 1))(*[at(100 + k) for k in range(n)])
+
+
+def spec(max_norm=1.0, eps=1e-6, inv=1.0, out=at(90)):
+    return ctypes.byref(zs.ClipSpec(max_norm, eps, inv, out))
+
+
+BAD_SPECS = [dict(max_norm=-1.0), dict(max_norm=NAN), dict(eps=-1e-9), dict(eps=INF), dict(eps=NAN),
+             dict(inv=0.0), dict(inv=-1.0), dict(inv=INF), dict(inv=NAN), dict(out=None)]
+
+
+# ---------------------------------------------------------------- workspace
+
+def test_workspace_sizes():
+    assert zs.zero_norm_workspace() == 8 * zs.ZERO_NORM_PARTIALS
+    assert zs.zero_norm_workspace(zs.ZERO_NORM_PARTIALS + 1) == 8 * (zs.ZERO_NORM_PARTIALS + 1)
+    for bad in (-1, 1 << 31):
+        with pytest.raises(zs.ZeroShardError):
+            zs.zero_norm_workspace(bad)
+
+
+# ---------------------------------------------------------------- the reduce
+
+def reduce_norm(p=None, n_ranks=4, gdt=0, rs=None, n=1000, out=at(1), sq=at(2), sp=None, ws=at(3),
+                ws_bytes=1 << 20):
+    return zs.raw_call("zero_reduce_norm_shard", parts(n_ranks) if p is None else p, n_ranks, gdt, rs,
+                       n, out, sq, sp, ws, ws_bytes, None)
+
+
+def rspec(group=0, micro=1, acc=None):
+    return ctypes.byref(zs.ReduceSpec(group, micro, acc))
+
+
+def test_reduce_norm_refusals():
+    assert reduce_norm() == NOT_DEVICE
+    assert reduce_norm(out=None) == NOT_DEVICE           # the norm alone
+    assert reduce_norm(sp=spec()) == NOT_DEVICE
+    assert reduce_norm(rs=rspec(2, 3, at(5))) == NOT_DEVICE
+    assert reduce_norm(rs=rspec(0, 3, at(1))) == NOT_DEVICE   # grad_out is the accumulator
+    for bad in (dict(n_ranks=0), dict(n_ranks=65), dict(n=-1), dict(n=(1 << 48) + 1), dict(sq=None),
+                dict(ws=None), dict(ws_bytes=-1), dict(rs=rspec(3)), dict(rs=rspec(0, 2)),
+                dict(rs=rspec(0, 1, at(5))), dict(rs=rspec(0, 0))):
+        assert reduce_norm(**bad) == INVALID, bad
+    for bad in BAD_SPECS:
+        assert reduce_norm(sp=spec(**bad)) == INVALID, bad
+    holed = parts(4)
+    holed[2] = None
+    assert reduce_norm(p=holed) == INVALID
+    assert reduce_norm(ws_bytes=zs.zero_norm_workspace() - 1) == CAPACITY
+    crooked = parts(4)
+    crooked[3] = at(103) + 8
+    for bad in (dict(p=crooked), dict(out=at(1) + 4), dict(sq=at(2) + 4), dict(ws=at(3) + 8),
+                dict(sp=spec(out=at(90) + 8)), dict(rs=rspec(0, 2, at(5) + 4))):
+        assert reduce_norm(**bad) == MISALIGNED, bad
+    for gdt in (2, 3, -1):                                # fp16 is for pieces alone
+        assert reduce_norm(gdt=gdt) == UNSUPPORTED
+    for bad in (dict(out=at(100) + 1984), dict(sq=at(100) + 8), dict(sq=at(1) + 8), dict(ws=at(1) + 16),
+                dict(ws=at(2) - 16), dict(sp=spec(out=at(2))), dict(sp=spec(out=at(101))),
+                dict(rs=rspec(0, 2, at(1) + 16)), dict(rs=rspec(0, 2, at(3) + 160)),
+                dict(rs=rspec(0, 2, at(2) - 16))):
+        assert reduce_norm(**bad) == ALIAS, bad
+
+
+# ---------------------------------------------------------------- the coefficient
+
+def test_clip_coef_refusals():
+    call = lambda sq=at(2), n=4, sp=spec(): zs.raw_call("zero_clip_coef", sq, n, sp, None)
+    assert call() == NOT_DEVICE
+    assert call(sp=spec(max_norm=INF)) == NOT_DEVICE      # never clips
+    assert call(sp=spec(max_norm=0.0, eps=0.0)) == NOT_DEVICE
+    for bad in (dict(sq=None), dict(n=0), dict(n=-1), dict(n=1 << 31), dict(sp=None)):
+        assert call(**bad) == INVALID, bad
+    for bad in BAD_SPECS:
+        assert call(sp=spec(**bad)) == INVALID, bad
+    assert call(sq=at(2) + 4) == MISALIGNED
+    assert call(sp=spec(out=at(90) + 8)) == MISALIGNED
+    assert call(sp=spec(out=at(2) + 16)) == ALIAS
+    assert call(sp=spec(out=at(2) + 32)) == NOT_DEVICE
+
+
+# ---------------------------------------------------------------- the clipped steps
+
+STEPS = ["zero_shard_step", "zero_shard_step_bf16_moments", "zero_shard_step_kahan"]
+
+
+def clipped(name, sched, n_ranks=1, gdt=1, first=at(1), m=at(2), v=at(3), n=1000, chunks=at(4), n_chunks=1,
+            hp=None, consts=at(5), n_consts=4, index=at(6), clip=at(7)):
+    how = (consts, n_consts, index) if sched else (ctypes.byref(hp or zs.hparams(1)),)
+    return zs.raw_call(name + ("_scheduled" if sched else "") + "_clipped", parts(n_ranks), n_ranks, gdt,
+                       first, m, v, n, chunks, n_chunks, *how, clip, None)
+
+
+@pytest.mark.parametrize("sched", [False, True])
+@pytest.mark.parametrize("name", STEPS)
+def test_clipped_step_refusals(name, sched):
+    call = lambda **k: clipped(name, sched, **k)
+    assert call() == NOT_DEVICE
+    assert call(clip=None) == INVALID
+    assert call(clip=at(7) + 8) == MISALIGNED
+    assert call(clip=at(2)) == ALIAS and call(clip=at(3) + 1984) == ALIAS and call(clip=at(1) + 16) == ALIAS
+    # and what the step it is named after refuses
+    assert call(n_ranks=65) == INVALID and call(first=None) == INVALID and call(n=-1) == INVALID
+    assert call(chunks=None) == INVALID and call(m=at(2) + 8) == MISALIGNED and call(gdt=2) == UNSUPPORTED
+    assert call(m=at(3)) == ALIAS and call(v=at(100)) == ALIAS
+    if sched:
+        assert call(consts=None) == INVALID and call(index=at(6) + 4) == MISALIGNED
+        assert call(index=at(1) + 8) == ALIAS
+    else:
+        assert call(hp=zs.hparams(0)) == INVALID
+    assert call(n=0, clip=None, first=None, m=None, v=None, chunks=None, n_chunks=0) == zs.ZERO_OK
+    assert call(n_chunks=0, chunks=None) == zs.ZERO_OK
+
+
+# ---------------------------------------------------------------- many tensors
+
+def test_norm_pieces_refusals():
+    def call(pieces=at(1), n=10, sq=at(2), tsq=at(3), n_tensors=5, sp=None, ws=at(4), ws_bytes=1 << 20):
+        return zs.raw_call("zero_norm_pieces", pieces, n, sq, tsq, n_tensors, sp, ws, ws_bytes, None)
+    assert call() == NOT_DEVICE and call(tsq=None, n_tensors=0) == NOT_DEVICE and call(sp=spec()) == NOT_DEVICE
+    for bad in (dict(pieces=None), dict(n=-1), dict(n=1 << 31), dict(sq=None), dict(ws=None),
+                dict(n_tensors=-1), dict(n_tensors=1 << 31), dict(ws_bytes=-8)):
+        assert call(**bad) == INVALID, bad
+    for bad in BAD_SPECS:
+        assert call(sp=spec(**bad)) == INVALID, bad
+    assert call(n=200000) == CAPACITY
+    for bad in (dict(pieces=at(1) + 8), dict(sq=at(2) + 4), dict(tsq=at(3) + 4), dict(ws=at(4) + 8),
+                dict(sp=spec(out=at(9) + 8))):
+        assert call(**bad) == MISALIGNED, bad
+    for bad in (dict(sq=at(3) + 32), dict(tsq=at(1) + 312), dict(ws=at(1) + 304), dict(sq=at(4) + 8),
+                dict(sp=spec(out=at(3) + 32)), dict(sp=spec(out=at(2)))):
+        assert call(**bad) == ALIAS, bad
+
+
+def test_scale_pieces_refusals():
+    call = lambda p=at(1), n=10, c=at(2): zs.raw_call("zero_scale_pieces", p, n, c, None)
+    assert call() == NOT_DEVICE
+    assert call(p=None) == INVALID and call(n=-1) == INVALID and call(n=1 << 31) == INVALID and call(c=None) == INVALID
+    assert call(p=at(1) + 8) == MISALIGNED and call(c=at(2) + 8) == MISALIGNED
+    assert call(p=None, n=0) == zs.ZERO_OK
+
+
+def build(src, sdt, numels, dst=None, ddt=None, max_piece=128, cap=None):
+    n = len(numels)
+    pv, iv = ctypes.c_void_p * max(n, 1), ctypes.c_int * max(n, 1)
+    nm = np.array(numels + [0], dtype=np.int64)
+    args = (None if src is None else pv(*src), None if sdt is None else iv(*sdt),
+            None if dst is None else pv(*dst), None if ddt is None else iv(*ddt), nm.ctypes.data, n, max_piece)
+    count = ctypes.c_int64(-7)
+    rc = zs.raw_call("zero_build_pieces", *args, None, 0, ctypes.byref(count))
+    if rc:
+        return rc, None
+    out = np.zeros(count.value if cap is None else cap, dtype=zs.PIECE_DTYPE)
+    rc = zs.raw_call("zero_build_pieces", *args, out.ctypes.data, len(out), ctypes.byref(count))
+    return rc, out
+
+
+def test_build_pieces_refusals():
+    a, b = at(1), at(2)
+    assert build([a, b], [0, 1], [10, 10])[0] == zs.ZERO_OK
+    for bad in (dict(src=None, sdt=[0], numels=[4]), dict(src=[a], sdt=None, numels=[4]),
+                dict(src=[a], sdt=[0], numels=[-1]), dict(src=[None], sdt=[0], numels=[4]),
+                dict(src=[a], sdt=[0], numels=[4], dst=[b]), dict(src=[a], sdt=[0], numels=[4], ddt=[0]),
+                dict(src=[a], sdt=[0], numels=[4], dst=[None], ddt=[0]),
+                dict(src=[a, b], sdt=[0, 0], numels=[1 << 48, 1]),
+                dict(src=[a], sdt=[0], numels=[4], max_piece=0), dict(src=[a], sdt=[0], numels=[4], max_piece=100),
+                dict(src=[a], sdt=[0], numels=[4], max_piece=(1 << 24) + 64)):
+        assert build(**bad)[0] == INVALID, bad
+    assert build([a + 1], [0], [4])[0] == MISALIGNED and build([a + 2], [1], [4])[0] == MISALIGNED
+    assert build([a], [0], [4], [b + 2], [1])[0] == MISALIGNED
+    assert build([a + 2], [2], [4])[0] == zs.ZERO_OK
+    assert build([a], [3], [4])[0] == UNSUPPORTED and build([a], [0], [4], [b], [-1])[0] == UNSUPPORTED
+    # places: another's place, another tensor, its own tensor shifted or in another type
+    assert build([a, a + 14], [0, 0], [8, 8])[0] == ALIAS
+    assert build([a, b], [0, 0], [8, 8], [at(3), at(3) + 14], [0, 0])[0] == ALIAS
+    assert build([a, b], [0, 0], [8, 8], [b + 14, at(3)], [0, 0])[0] == ALIAS
+    assert build([a], [0], [8], [a + 2], [0])[0] == ALIAS and build([a], [0], [8], [a], [2])[0] == ALIAS
+    assert build([a, b], [0, 0], [8, 8], [b, a], [0, 0])[0] == ALIAS
+    # exactly its own, the same tensor read twice into two places, and neighbours
+    assert build([a, b], [0, 0], [8, 8], [a, at(3)], [0, 1])[0] == zs.ZERO_OK
+    assert build([a, a], [0, 0], [8, 8], [b, at(3)], [0, 0])[0] == zs.ZERO_OK
+    assert build([a, a + 16], [0, 0], [8, 8])[0] == zs.ZERO_OK
+    assert build([a], [0], [300], cap=2)[0] == CAPACITY
+    assert build([], [], [])[0] == zs.ZERO_OK
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_pieces_cover_each_element_once_and_start_aligned(seed):
+    rng = np.random.default_rng(seed)
+    n = int(rng.integers(1, 30))
+    numels = [int(x) for x in rng.integers(0, 700, n)]
+    sdt = [int(x) for x in rng.integers(0, 3, n)]
+    ddt = [int(x) for x in rng.integers(0, 3, n)]
+    size = {0: 2, 1: 4, 2: 2}
+    src = [at(10 + t) + size[sdt[t]] * int(rng.integers(0, 16)) for t in range(n)]
+    dst = [at(60 + t) + size[ddt[t]] * int(rng.integers(0, 16)) for t in range(n)]
+    rc, tab = build(src, sdt, numels, dst, ddt, max_piece=128)
+    assert rc == zs.ZERO_OK
+    row = 0
+    for t in range(n):
+        first, got = row, 0
+        while row < len(tab) and tab[row]["tensor_id"] == t:
+            p = tab[row]
+            assert p["src"] == src[t] + got * size[sdt[t]] and p["dst"] == dst[t] + got * size[ddt[t]]
+            assert (p["src_dt"], p["dst_dt"]) == (sdt[t], ddt[t]) and p["len"] <= 128
+            assert row == first or (p["dst"] % 16 == 0 and p["len"] > 0)
+            got += int(p["len"])
+            row += 1
+        assert got == numels[t] and row > first
+        assert tab[first]["tensor_pieces"] == row - first
+        assert not tab["tensor_pieces"][first + 1:row].any()
+    assert row == len(tab)
+
+
+def test_the_binding_takes_dense_tensors_only():
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="device memory"):
+        zs.zero_build_pieces([torch.zeros(4)])
+
+    class Fake:
+        """The parts of a CUDA tensor that the checks look at."""
+        is_cuda, dtype = True, torch.float32
+
+        def __init__(self, t):
+            self.t, self.shape = t, t.shape
+            self.stride, self.is_contiguous, self.numel = t.stride, t.is_contiguous, t.numel
+
+        def data_ptr(self):
+            return at(1)
+
+    full = torch.zeros(6, 10, 4)
+    for t in (full, full.permute(2, 0, 1), full.transpose(0, 1), full[2:4], full[1:2, :, :].transpose(0, 2)):
+        assert zs.zero_build_pieces([Fake(t)])["len"].sum() == t.numel()
+    for t in (full[:, ::2], full[:, :5], full[0, 0, :1].expand(7), full.permute(2, 0, 1)[:, :, 1:]):
+        with pytest.raises(ValueError, match="gaps or overlaps"):
+            zs.zero_build_pieces([Fake(t)])
+    with pytest.raises(ValueError, match="dst must match"):
+        zs.zero_build_pieces([Fake(full)], [Fake(full.permute(2, 0, 1))])
+    with pytest.raises(ValueError, match="dst must match"):
+        zs.zero_build_pieces([Fake(full)], [])
+    assert len(zs.zero_build_pieces([])) == 0
+
+
+def test_scheduled_and_plain_clipped_steps_are_declared_together():
+    for name in STEPS:
+        for f in (name + "_clipped", name + "_scheduled_clipped"):
+            assert hasattr(zs, f) and hasattr(zs.lib(), f)

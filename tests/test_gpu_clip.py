@@ -1,0 +1,599 @@
+"""Clipping by the global norm on the GPU, against plain 64-bit arithmetic and
+the CPU oracle.
+
+Tolerances.  A sum of squares is a sum of non-negative doubles whose terms are
+exact, so its relative error is at most k 2^-53 with k the additions any term
+passes through: here at most 128 in a lane (a piece of 16384 elements, 64
+lanes, 4 sums a lane: 64; a lane of the reduce: 32 a span and at most 4 spans
+at these sizes), 8 over the lanes and 40 in the second launch, so 176 2^-53 <
+2e-14.  The norm is its square root (half the error, and two roundings), the
+coefficient a quotient of it (two more): 2e-14 holds for those too.  math.fsum
+rounds once.  Everything else is compared bit for bit: scaled values with the
+64-bit product rounded once, gradients and steps with the oracle, both from
+the coefficient that the device formed.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from gpu_helpers import assert_bitwise, say
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+SUM_TOL = 2e-14
+HP = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.1)
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def zs():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import sharded_optimizer_step_shard_amd as m
+    return m
+
+
+def dev(x):
+    a = np.ascontiguousarray(x)
+    return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).cuda()
+
+
+def host(t):
+    a = t.cpu().numpy()
+    return a.view(np.uint16) if a.dtype == np.int16 else a
+
+
+def bits_to_f64(h):
+    return (h.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def wide(x):
+    """Host array (uint16: bf16 bits) in 64 bits."""
+    return bits_to_f64(x) if x.dtype == np.uint16 else x.astype(np.float64)
+
+
+def want_clip(sq, max_norm, eps=EPS, inv=1.0):
+    norm = inv * math.sqrt(sq)
+    return norm, inv * min(1.0, max_norm / (norm + eps)) if norm + eps > 0 else inv
+
+
+def near(got, want, what):
+    if want == 0 or not math.isfinite(want):
+        assert got == want or (math.isnan(got) and math.isnan(want)), (what, got, want)
+    else:
+        assert abs(got - want) <= SUM_TOL * abs(want), (what, got, want)
+
+
+def f64(n=1, fill=-7.0):
+    return torch.full((n,), fill, dtype=torch.float64, device="cuda")
+
+
+def workspace(zs, n=0):
+    """Filled with NaN: nothing in it may be read before it is written."""
+    return f64(zs.zero_norm_workspace(n) // 8, float("nan"))
+
+
+def partials_of(rng, n, ranks, gdt, sigma=1e-3):
+    x = rng.standard_normal((ranks, n)).astype(np.float32) * np.float32(sigma)
+    return [oracle.bf16_round(r) if gdt == "bf16" else r.copy() for r in x]
+
+
+# ---------------------------------------------------------------- reduce with the norm
+
+@pytest.mark.parametrize("n", [1, 3, 7, 8, 9, 63, 64, 65, 511, 2047, 2048, 2049, 4097, 70001, 1000003])
+@pytest.mark.parametrize("gdt", ["bf16", "fp32"])
+def test_reduce_norm_sizes(zs, n, gdt):
+    say(f"case: reduce with norm, n={n} {gdt}")
+    rng = np.random.default_rng(n)
+    for ranks in (1, 3, 8):
+        p = partials_of(rng, n, ranks, gdt)
+        g, sq, clip = torch.full((n + 8,), -3.0, device="cuda"), f64(), f64(2)
+        zs.zero_reduce_norm_shard([dev(x) for x in p], n, sq, workspace(zs), grad_out=g, gdt=0 if gdt == "bf16" else 1,
+                                  spec=zs.clip_spec(clip, 1e-3, EPS, 0.5))
+        want = oracle.reduce(p)
+        assert_bitwise(host(g)[:n], want, f"gradient of {ranks}")
+        assert (host(g)[n:] == -3.0).all()
+        s = math.fsum((wide(want) ** 2).tolist())
+        near(sq.item(), s, "square")
+        norm, coef = want_clip(s, 1e-3, inv=0.5)
+        near(clip[0].item(), norm, "norm")
+        near(clip[1].item(), coef, "coef")
+
+
+@pytest.mark.parametrize("ranks,group,micro", [(2, 1, 1), (4, 2, 1), (6, 3, 2), (8, 4, 1), (8, 2, 3), (12, 4, 1), (16, 8, 4),
+                                               (16, 4, 1), (24, 8, 2), (32, 8, 1), (32, 16, 1), (64, 8, 1), (64, 0, 5), (5, 0, 1)])
+@pytest.mark.parametrize("gdt", ["bf16", "fp32"])
+def test_reduce_norm_orders_and_accumulators(zs, ranks, group, micro, gdt):
+    say(f"case: reduce with norm, {ranks} ranks group {group} micro {micro} {gdt}")
+    n = 6001
+    rng = np.random.default_rng(ranks + group)
+    p = partials_of(rng, n, ranks, gdt)
+    acc = rng.standard_normal(n).astype(np.float32) * np.float32(1e-2) if micro > 1 else None
+    want = oracle.reduce_ex(p, group or None, acc, micro)
+    d = [dev(x) for x in p]
+    code = 0 if gdt == "bf16" else 1
+    for place in ("own", "accumulator", "none"):
+        if place == "accumulator" and acc is None:
+            continue
+        d_acc = None if acc is None else dev(acc)
+        g = {"own": torch.empty(n, device="cuda"), "accumulator": d_acc, "none": None}[place]
+        sq = f64()
+        zs.zero_reduce_norm_shard(d, n, sq, workspace(zs), grad_out=g, group=group, micro_batches=micro, acc=d_acc, gdt=code)
+        near(sq.item(), math.fsum((wide(want) ** 2).tolist()), f"square, {place}")
+        if g is not None:
+            assert_bitwise(host(g), want, f"gradient, {place}")
+
+
+def test_reduce_norm_of_an_empty_shard_is_zero(zs):
+    sq, clip = f64(), f64(2)
+    zs.zero_reduce_norm_shard([0, 0], 0, sq, workspace(zs), gdt=0, spec=zs.clip_spec(clip, 1.0))
+    assert sq.item() == 0.0 and clip.tolist() == [0.0, 1.0]
+
+
+def test_reduce_norm_spans_more_than_one_to_a_wave(zs):
+    """Longer than ZERO_NORM_PARTIALS spans: waves take several, and the same
+    call gives the same bits again."""
+    n = zs.ZERO_NORM_PARTIALS * 2048 + 12345
+    x = torch.empty(n, device="cuda").normal_(0, 1e-3, generator=torch.Generator("cuda").manual_seed(1))
+    sq, again, g = f64(), f64(), torch.empty(n, device="cuda")
+    zs.zero_reduce_norm_shard([x], n, sq, workspace(zs), grad_out=g)
+    zs.zero_reduce_norm_shard([x], n, again, workspace(zs))
+    assert torch.equal(g, x) and sq.item() == again.item()
+    near(sq.item(), math.fsum(np.square(x.cpu().numpy().astype(np.float64)).reshape(-1).tolist()), "square")
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_a_norm_that_is_not_finite(zs, value):
+    n = 5000
+    x = torch.full((n,), 1e-3, device="cuda")
+    x[n - 1] = value
+    sq, clip = f64(), f64(2)
+    zs.zero_reduce_norm_shard([x], n, sq, workspace(zs), spec=zs.clip_spec(clip, 1.0))
+    assert not math.isfinite(sq.item()) and not math.isfinite(clip[0].item()) and math.isnan(clip[1].item())
+
+
+def test_squares_beyond_fp32(zs):
+    """fp32's largest and smallest values: their squares are in range."""
+    n = 4096
+    x = torch.full((n,), 3.0e38, device="cuda")
+    sq, clip = f64(), f64(2)
+    zs.zero_reduce_norm_shard([x], n, sq, workspace(zs), spec=zs.clip_spec(clip, 1.0))
+    s = math.fsum([float(np.float32(3.0e38)) ** 2] * n)
+    near(sq.item(), s, "large")
+    near(clip[1].item(), want_clip(s, 1.0)[1], "coef")
+    x.fill_(1e-45)
+    zs.zero_reduce_norm_shard([x], n, sq, workspace(zs))
+    near(sq.item(), n * float(np.float32(1e-45)) ** 2, "subnormal")
+
+
+# ---------------------------------------------------------------- the coefficient
+
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 1000])
+def test_clip_coef(zs, n):
+    rng = np.random.default_rng(n)
+    x = rng.random(n)
+    s = math.fsum(x.tolist())
+    clip = f64(2)
+    for max_norm, eps, inv in ((0.5, EPS, 1.0), (1e6, EPS, 1.0), (float("inf"), EPS, 1 / 1024), (0.0, EPS, 1.0),
+                               (0.25 * math.sqrt(s), 0.0, 1 / 3)):
+        zs.zero_clip_coef(dev(x), n, zs.clip_spec(clip, max_norm, eps, inv))
+        norm, coef = want_clip(s, max_norm, eps, inv)
+        near(clip[0].item(), norm, "norm")
+        near(clip[1].item(), coef, "coef")
+        if max_norm >= 1e6:
+            assert clip[1].item() == inv      # exactly: nothing is clipped
+    # the border: a norm of exactly max_norm is left alone, eps counts
+    clip.fill_(-1)
+    zs.zero_clip_coef(dev(np.array([4.0])), 1, zs.clip_spec(clip, 2.0, 0.0))
+    assert clip.tolist() == [2.0, 1.0]
+    zs.zero_clip_coef(dev(np.array([4.0])), 1, zs.clip_spec(clip, 2.0, 2.0))
+    assert clip.tolist() == [2.0, 0.5]
+    zs.zero_clip_coef(dev(np.zeros(3)), 3, zs.clip_spec(clip, 0.0, 0.0))
+    assert clip.tolist() == [0.0, 1.0]
+
+
+# ---------------------------------------------------------------- many tensors
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def tensors(rng, numels, kinds, skew=0):
+    """Tensors packed one after another, each `skew` elements after the last."""
+    out = []
+    for n, k in zip(numels, kinds):
+        t = torch.from_numpy(rng.standard_normal(n + skew).astype(np.float32)).to(DT[k]).cuda()
+        out.append(t[skew:])
+    return out
+
+
+def t64(t):
+    return t.detach().to("cpu", torch.float64).reshape(-1).numpy()
+
+
+def rounded(y64, kind):
+    """64-bit values to the type's bits in one rounding."""
+    if kind == "bf16":
+        return oracle.bf16_from_double(y64)
+    with np.errstate(over="ignore"):
+        return y64.astype(np.float16 if kind == "fp16" else np.float32)
+
+
+def t_bits(t):
+    t = t.detach().reshape(-1).cpu()
+    return t.view(torch.int16).numpy().view(np.uint16) if t.dtype == torch.bfloat16 else t.numpy()
+
+
+def same_bits(got, want, what):
+    kind = np.uint32 if want.dtype == np.float32 else np.uint16
+    a, b = np.ascontiguousarray(got).view(kind), np.ascontiguousarray(want).view(kind)
+    assert np.array_equal(a, b), (what, int((a != b).sum()), a.size, int(np.nonzero(a != b)[0][0]))
+
+
+SHAPES = {"one": [1], "tiny": [1, 2, 3, 0, 5, 8, 7, 9, 0], "odd": [4095, 1, 64, 70001, 513, 0, 16384, 16385, 33],
+          "long": [300007], "many": [17] * 700}
+
+
+@pytest.mark.parametrize("kinds", ["bf16", "fp16", "fp32", "mixed"])
+@pytest.mark.parametrize("shape", sorted(SHAPES))
+def test_norm_of_many_tensors(zs, shape, kinds):
+    say(f"case: norm of tensors, {shape} {kinds}")
+    rng = np.random.default_rng(5)
+    numels = SHAPES[shape]
+    names = [("bf16", "fp16", "fp32")[i % 3] if kinds == "mixed" else kinds for i in range(len(numels))]
+    for skew in (0, 1, 5):
+        ts = tensors(rng, numels, names, skew)
+        table = zs.zero_build_pieces(ts)
+        sq, tsq, clip = f64(), f64(len(ts) + 1), f64(2)
+        zs.zero_norm_pieces(zs.pieces_to_device(table), len(table), sq, workspace(zs, len(table)), tensor_sq=tsq[:-1],
+                            spec=zs.clip_spec(clip, 2.0, EPS, 0.125))
+        each = [math.fsum((t64(t) ** 2).tolist()) for t in ts]
+        for i, e in enumerate(each):
+            near(tsq[i].item(), e, f"tensor {i}")
+        assert tsq[-1].item() == -7.0
+        s = math.fsum(each)
+        near(sq.item(), s, "all")
+        norm, coef = want_clip(s, 2.0, inv=0.125)
+        near(clip[0].item(), norm, "norm")
+        near(clip[1].item(), coef, "coef")
+
+
+@pytest.mark.parametrize("max_piece", [64, 128, 4096])
+def test_norm_in_other_piece_lengths_and_runs(zs, max_piece):
+    rng = np.random.default_rng(6)
+    ts = tensors(rng, [1000, 7, 9999, 0, 4096], ["bf16", "fp32", "fp16", "fp32", "bf16"], 3)
+    table = zs.zero_build_pieces(ts, max_piece=max_piece)
+    d = zs.pieces_to_device(table)
+    each = [math.fsum((t64(t) ** 2).tolist()) for t in ts]
+    sq, tsq = f64(), f64(len(ts))
+    zs.zero_norm_pieces(d, len(table), sq, workspace(zs, len(table)), tensor_sq=tsq)
+    near(sq.item(), math.fsum(each), "all")
+    for i, e in enumerate(each):
+        near(tsq[i].item(), e, f"tensor {i}")
+    # tensors 2 and on alone: a run of the table
+    first = int(np.nonzero(table["tensor_id"] == 2)[0][0])
+    tsq.fill_(-7)
+    zs.zero_norm_pieces(d.data_ptr() + 32 * first, len(table) - first, sq, workspace(zs, len(table)), tensor_sq=tsq)
+    near(sq.item(), math.fsum(each[2:]), "run")
+    assert tsq[:2].tolist() == [-7.0, -7.0]
+    # fewer tensors' sums than the table names: the rest is left out
+    tsq.fill_(-7)
+    zs.zero_norm_pieces(d, len(table), sq, workspace(zs, len(table)), tensor_sq=tsq[:2])
+    near(tsq[1].item(), each[1], "second")
+    assert tsq[2:].tolist() == [-7.0] * 3
+    near(sq.item(), math.fsum(each), "all again")
+
+
+def test_norm_of_an_empty_table_is_zero(zs):
+    sq, clip = f64(), f64(2)
+    zs.zero_norm_pieces(None, 0, sq, workspace(zs), spec=zs.clip_spec(clip, 1.0))
+    assert sq.item() == 0.0 and clip.tolist() == [0.0, 1.0]
+    zs.zero_scale_pieces(None, 0, clip)
+
+
+def test_norm_skips_malformed_pieces(zs):
+    ts = tensors(np.random.default_rng(7), [500, 600, 700], ["bf16"] * 3)
+    table = zs.zero_build_pieces(ts)
+    table["len"][0], table["src_dt"][1] = -5, 9
+    table["dst_dt"][2] = 9
+    d = zs.pieces_to_device(table)
+    sq = f64()
+    zs.zero_norm_pieces(d, 3, sq, workspace(zs, 3))
+    near(sq.item(), math.fsum((t64(ts[2]) ** 2).tolist()), "the third alone")
+    before = [t.clone() for t in ts]
+    zs.zero_scale_pieces(d, 3, torch.tensor([1.0, 0.5], dtype=torch.float64, device="cuda"))
+    assert all(torch.equal(a, b) for a, b in zip(before, ts))
+
+
+@pytest.mark.parametrize("to", ["same", "bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("kinds", ["bf16", "fp16", "fp32", "mixed"])
+def test_scale_into_other_places(zs, kinds, to):
+    say(f"case: scaling {kinds} to {to}")
+    rng = np.random.default_rng(8)
+    numels = [1, 7, 8, 9, 0, 15, 64, 513, 4097, 20011]
+    names = [("bf16", "fp16", "fp32")[i % 3] if kinds == "mixed" else kinds for i in range(len(numels))]
+    into = names if to == "same" else [to] * len(numels)
+    for skew, dskew in ((0, 0), (1, 0), (0, 3), (5, 7), (2, 2)):
+        ts = tensors(rng, numels, names, skew)
+        outs = [torch.full((n + dskew + 9,), -2.0, dtype=DT[k], device="cuda") for n, k in zip(numels, into)]
+        places = [o[dskew:dskew + n] for o, n in zip(outs, numels)]
+        table = zs.zero_build_pieces(ts, places, max_piece=4096)
+        for coef in (1.0 / 3, 1.0, 1e-3, 0.0, 300.0):
+            clip = torch.tensor([5.0, coef], dtype=torch.float64, device="cuda")
+            zs.zero_scale_pieces(zs.pieces_to_device(table), len(table), clip)
+            for t, o, p, k in zip(ts, outs, places, into):
+                same_bits(t_bits(p), rounded(coef * t64(t), k), (skew, dskew, coef, k, t.numel()))
+                assert (o[:dskew] == -2).all() and (o[dskew + t.numel():] == -2).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_scale_every_rounding(zs, kind):
+    """Every finite bf16 and fp16 pattern (a spread of fp32 ones), by a
+    coefficient that takes some below the normal numbers and some to halves."""
+    if kind == "fp32":
+        bits = np.arange(0, 1 << 32, 65521, dtype=np.uint64).astype(np.uint32)
+        x = torch.from_numpy(bits.view(np.int32)).view(torch.float32)
+    else:
+        x = torch.from_numpy(np.arange(1 << 16, dtype=np.uint16).view(np.int16)).view(DT[kind])
+    x = x[torch.isfinite(x)].cuda()
+    for coef in (0.75, 0.1, 2.0 ** -20 * 1.5, 2.0 ** 12):
+        for to in ("bf16", "fp16", "fp32"):
+            out = torch.empty(x.numel(), dtype=DT[to], device="cuda")
+            table = zs.zero_build_pieces([x], [out])
+            zs.zero_scale_pieces(zs.pieces_to_device(table), len(table), torch.tensor([0.0, coef], dtype=torch.float64, device="cuda"))
+            same_bits(t_bits(out), rounded(coef * t64(x), to), (kind, to, coef))
+
+
+def test_scale_in_place_and_permuted(zs):
+    rng = np.random.default_rng(9)
+    a = torch.from_numpy(rng.standard_normal((40, 30, 20)).astype(np.float32)).cuda()
+    b = a.bfloat16().permute(2, 0, 1)
+    c = a.half()[3:7]
+    ts = [a.transpose(0, 1), b, c]
+    want = [0.3 * t64(t) for t in ts]
+    table = zs.zero_build_pieces(ts)
+    clip = torch.tensor([0.0, 0.3], dtype=torch.float64, device="cuda")
+    zs.zero_scale_pieces(zs.pieces_to_device(table), len(table), clip)
+    for t, w, k in zip(ts, want, ("fp32", "bf16", "fp16")):
+        same_bits(t_bits(t), rounded(w, k), k)
+
+
+def test_a_nan_coefficient_changes_nothing(zs):
+    ts = tensors(np.random.default_rng(10), [1000, 77], ["bf16", "fp32"])
+    outs = [torch.full_like(t, 4.0) for t in ts]
+    clip = f64(2, float("nan"))
+    for dst in (None, outs):
+        table = zs.zero_build_pieces(ts, dst)
+        before = [t.clone() for t in ts]
+        zs.zero_scale_pieces(zs.pieces_to_device(table), len(table), clip)
+        assert all(torch.equal(x, y) for x, y in zip(ts, before))
+    assert all((o == 4.0).all() for o in outs)
+
+
+# ---------------------------------------------------------------- the clipped steps
+
+def bf16_bits(rng, n, sigma):
+    return oracle.bf16_round((rng.standard_normal(n) * sigma).astype(np.float32))
+
+
+def state_of(layout, rng, n):
+    """(host state arrays, bf16 parameters)"""
+    prm = bf16_bits(rng, n, 0.02)
+    if layout == "kahan":
+        return [bf16_bits(rng, n, 1e-5), bf16_bits(rng, n, 1e-4), oracle.bf16_round(rng.random(n).astype(np.float32) * 1e-8)], prm
+    th = (rng.standard_normal(n) * 0.02).astype(np.float32)
+    if layout == "bf16m":
+        return [th, bf16_bits(rng, n, 1e-4), oracle.bf16_round(rng.random(n).astype(np.float32) * 1e-8)], prm
+    return [th, (rng.standard_normal(n) * 1e-4).astype(np.float32), (rng.random(n) * 1e-8).astype(np.float32)], prm
+
+
+def oracle_step(layout, g, st, prm, t):
+    hp = oracle.hparams(t, **HP)
+    if layout == "kahan":
+        th, c, m, v = oracle.shard_step_kahan([g], prm, *st, hp)
+        return [c, m, v], th
+    f = oracle.shard_step if layout == "fp32" else oracle.shard_step_bf16m
+    th, m, v, p = f([g], *st, hp)
+    return [th, m, v], p
+
+
+NAMES = {"fp32": "zero_shard_step", "bf16m": "zero_shard_step_bf16_moments", "kahan": "zero_shard_step_kahan"}
+
+
+class Shard:
+    """One rank's device buffers, its parameters `skew` elements into a slot."""
+
+    def __init__(self, zs, layout, n, skew=0, max_chunk=None, seed=0):
+        self.zs, self.layout, self.n = zs, layout, n
+        self.st, self.prm = state_of(layout, np.random.default_rng(seed), n)
+        self.d = [dev(x) for x in self.st]
+        self.slot = torch.full((n + skew + 16,), 7, dtype=torch.int16, device="cuda")
+        self.skew = skew
+        self.slot[skew:skew + n] = dev(self.prm)
+        table, _ = zs.zero_build_chunks([n], 1, 0, slot_dst=self.slot.data_ptr() + 2 * skew,
+                                        max_chunk=max_chunk or zs.ZERO_DEFAULT_MAX_CHUNK_REDUCED)
+        self.n_chunks, self.chunks = len(table), zs.chunks_to_device(table)
+
+    def step(self, partials, clip, t=3, gdt=None):
+        getattr(self.zs, NAMES[self.layout] + "_clipped")(partials, *self.d, self.n, self.chunks, self.n_chunks,
+                                                          self.zs.hparams(t, **HP), clip, gdt=gdt)
+
+    def check(self, want, prm, what):
+        for i, (a, b) in enumerate(zip(self.d, want)):
+            assert_bitwise(host(a), b, f"{what} state {i}")
+        got = host(self.slot)
+        assert_bitwise(got[self.skew:self.skew + self.n], prm, f"{what} param")
+        assert (got[:self.skew] == 7).all() and (got[self.skew + self.n:] == 7).all(), what
+
+
+@pytest.mark.parametrize("n,skew", [(1, 0), (5, 1), (64, 0), (1023, 3), (4096, 0), (70001, 5)])
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_clipped_step_from_the_reduced_gradient(zs, layout, n, skew):
+    say(f"case: clipped step {layout} n={n} skew={skew}")
+    rng = np.random.default_rng(n)
+    g = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+    for coef in (0.3, 1.0, 0.0):
+        s = Shard(zs, layout, n, skew)
+        s.step([dev(g)], torch.tensor([9.0, coef], dtype=torch.float64, device="cuda"))
+        gc = (g.astype(np.float64) * coef).astype(np.float32)
+        s.check(*oracle_step(layout, gc, s.st, s.prm, 3), f"coef {coef}")
+
+
+@pytest.mark.parametrize("ranks", [2, 3, 4, 8, 16, 32, 64])
+@pytest.mark.parametrize("gdt", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_clipped_step_from_the_partials(zs, layout, gdt, ranks):
+    say(f"case: clipped step {layout} {ranks} ranks {gdt}")
+    n = 5003
+    p = partials_of(np.random.default_rng(ranks), n, ranks, gdt)
+    s = Shard(zs, layout, n, 3, max_chunk=2048)
+    s.step([dev(x) for x in p], torch.tensor([9.0, 0.7], dtype=torch.float64, device="cuda"), gdt=0 if gdt == "bf16" else 1)
+    gc = (oracle.reduce(p).astype(np.float64) * 0.7).astype(np.float32)
+    s.check(*oracle_step(layout, gc, s.st, s.prm, 3), "from partials")
+
+
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_coefficient_one_is_the_step_that_does_not_clip(zs, layout):
+    """Over enough chunks for the large-launch kernels of every layout."""
+    n = 1024 * (zs.ZERO_SMALL_LAUNCH_CHUNKS_12B + 3) + 77
+    g = torch.empty(n, device="cuda").normal_(0, 1e-3)
+    a, b = Shard(zs, layout, n), Shard(zs, layout, n)
+    a.step([g], torch.tensor([9.0, 1.0], dtype=torch.float64, device="cuda"))
+    getattr(zs, NAMES[layout])([g], *b.d, n, b.chunks, b.n_chunks, zs.hparams(3, **HP))
+    for x, y in zip(a.d + [a.slot], b.d + [b.slot]):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_a_step_whose_norm_is_not_finite_is_skipped(zs, layout):
+    s = Shard(zs, layout, 3001, 1)
+    g = torch.full((3001,), 1e-3, device="cuda")
+    g[5] = float("inf")
+    sq, clip = f64(), f64(2)
+    zs.zero_reduce_norm_shard([g], 3001, sq, workspace(zs), spec=zs.clip_spec(clip, 1.0))
+    s.step([g], clip)
+    s.check(s.st, s.prm, "skipped")
+
+
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_scheduled_clipped_step_in_a_graph(zs, layout):
+    """A whole clipped step captured once and replayed: other gradients, the
+    next constants and another coefficient on every replay, eager work and a
+    second captured step on the same workspace in between."""
+    n, ranks, steps = 30011, 4, 4
+    hps = [zs.hparams(t, **dict(HP, lr=1e-3 / t)) for t in range(1, steps + 1)]
+    consts = torch.from_numpy(zs.zero_make_step_consts(hps).view(np.uint8).copy()).cuda()
+    ws = workspace(zs)
+
+    class Job:
+        def __init__(self, seed):
+            self.s = Shard(zs, layout, n, 2, seed=seed)
+            self.index = torch.zeros(1, dtype=torch.int64, device="cuda")
+            self.parts = [torch.zeros(n, dtype=torch.int16, device="cuda") for _ in range(ranks)]
+            self.g, self.sq, self.clip = torch.empty(n, device="cuda"), f64(2), f64(2)
+            self.want, self.prm = [x.copy() for x in self.s.st], self.s.prm.copy()
+
+        def run(self):
+            zs.zero_reduce_norm_shard(self.parts, n, self.sq[:1], ws, grad_out=self.g, gdt=0)
+            zs.zero_clip_coef(self.sq, 2, zs.clip_spec(self.clip, 0.05))
+            getattr(zs, NAMES[layout] + "_scheduled_clipped")([self.g], *self.s.d, n, self.s.chunks, self.s.n_chunks, consts,
+                                                              steps, self.index, self.clip)
+            zs.zero_step_index_advance(self.index, steps)
+
+    jobs = [Job(1), Job(2)]
+    graphs = []
+    for j in jobs:
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(graph, stream=side):
+            j.run()
+        torch.cuda.current_stream().wait_stream(side)
+        graphs.append(graph)
+    rng = np.random.default_rng(3)
+    for t in range(1, steps + 2):            # the last replay is past the schedule: nothing changes
+        for j, graph in zip(jobs, graphs):
+            p = [bf16_bits(rng, n, 1e-3) for _ in range(ranks)]
+            other = float(rng.random()) * 1e-2
+            for d, x in zip(j.parts, p):
+                d.copy_(dev(x))
+            j.sq.fill_(other)
+            if t == 3:
+                j.parts[0][11] = 0x7F80      # an infinity: this step is skipped, and counted
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            if t <= steps and t != 3:
+                g = oracle.reduce(p)
+                s = math.fsum((wide(g) ** 2).tolist()) + other
+                norm, coef = j.clip.tolist()
+                near(norm, want_clip(s, 0.05)[0], "norm")
+                near(coef, want_clip(s, 0.05)[1], "coef")
+                assert coef < 1.0
+                hp = dict(HP, lr=1e-3 / t)
+                gc = (g.astype(np.float64) * coef).astype(np.float32)
+                o = oracle.hparams(t, **hp)
+                if layout == "kahan":
+                    j.prm, *j.want = oracle.shard_step_kahan([gc], j.prm, *j.want, o)
+                else:
+                    f = oracle.shard_step if layout == "fp32" else oracle.shard_step_bf16m
+                    *j.want, j.prm = f([gc], *j.want, o)
+            j.s.check(j.want, j.prm, f"replay {t}")
+            assert j.index.item() == min(t, steps)
+
+
+# ---------------------------------------------------------------- used together
+
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_ranks_of_a_model_clip_alike(zs, layout):
+    """Three ranks' shards of one ragged model (the last shorter, its slot odd):
+    squares gathered, one coefficient on all, every shard stepped; against the
+    oracle on the whole flat gradient."""
+    numels = [1000, 7, 4093, 64, 2903]
+    ranks, total = 3, sum(numels)
+    S = -(-total // ranks)
+    rng = np.random.default_rng(12)
+    full = [bf16_bits(rng, total, 1e-3) for _ in range(ranks)]
+    squares, jobs = f64(ranks), []
+    for r in range(ranks):
+        lo, hi = r * S, min((r + 1) * S, total)
+        s = Shard(zs, layout, hi - lo, r, seed=r)
+        g = torch.empty(hi - lo, device="cuda")
+        zs.zero_reduce_norm_shard([dev(p[lo:hi].copy()) for p in full], hi - lo, squares[r:r + 1], workspace(zs), grad_out=g, gdt=0)
+        jobs.append((lo, hi, s, g))
+    clip = f64(2)
+    zs.zero_clip_coef(squares, ranks, zs.clip_spec(clip, 0.01))
+    g = oracle.reduce(full)
+    norm, coef = clip.tolist()
+    near(norm, math.sqrt(math.fsum((wide(g) ** 2).tolist())), "norm")
+    gc = (g.astype(np.float64) * coef).astype(np.float32)
+    for lo, hi, s, d in jobs:
+        s.step([d], clip)
+        s.check(*oracle_step(layout, gc[lo:hi].copy(), s.st, s.prm, 3), f"shard at {lo}")
+        # the same through the calls over tensors: clip the gradient, then the step that does not
+        b = Shard(zs, layout, hi - lo, s.skew, seed=lo // S)
+        table = zs.zero_build_pieces([d])
+        zs.zero_scale_pieces(zs.pieces_to_device(table), len(table), clip)
+        getattr(zs, NAMES[layout])([d], *b.d, hi - lo, b.chunks, b.n_chunks, zs.hparams(3, **HP))
+        assert all(torch.equal(x, y) for x, y in zip(s.d + [s.slot], b.d + [b.slot]))
+
+
+def test_clipping_many_tensors_on_a_stream_of_its_own(zs):
+    """Norm, coefficient and scaling back to back on a stream that is not
+    torch's current one, against torch's definition on the host."""
+    rng = np.random.default_rng(13)
+    ts = tensors(rng, [50000, 3, 777, 20001], ["bf16", "fp32", "fp16", "bf16"], 1)
+    want = [t64(t) for t in ts]
+    table = zs.zero_build_pieces(ts)
+    d, ws, sq, clip = zs.pieces_to_device(table), workspace(zs, len(table)), f64(), f64(2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    zs.zero_norm_pieces(d, len(table), sq, ws, spec=zs.clip_spec(clip, 1.0, inv_scale=0.5), stream=side)
+    zs.zero_scale_pieces(d, len(table), clip, stream=side)
+    side.synchronize()
+    norm, coef = want_clip(math.fsum(x for w in want for x in (w * w).tolist()), 1.0, inv=0.5)
+    near(clip[0].item(), norm, "norm")
+    near(clip[1].item(), coef, "coef")
+    for t, w, k in zip(ts, want, ("bf16", "fp32", "fp16", "bf16")):
+        same_bits(t_bits(t), rounded(clip[1].item() * w, k), k)
