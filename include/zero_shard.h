@@ -199,8 +199,10 @@ enum {
  * ZERO_FP32), and piece length for the calls over many tensors. */
 #define ZERO_DEFAULT_MAX_CHUNK_REDUCED 1024
 #define ZERO_DEFAULT_MAX_PIECE 16384
-/* Partial sums zero_reduce_norm_shard leaves in its workspace, at most. */
-#define ZERO_NORM_PARTIALS 16384
+/* Partial sums zero_reduce_norm_shard leaves in its workspace, at most: one a
+ * wave, and a wave of its fastest shape takes 512 elements of bf16 or 256 of
+ * fp32, so that shards up to 2^30 (2^29) elements run in that shape. */
+#define ZERO_NORM_PARTIALS 2097152
 
 /*
  * Shard geometry and the chunk table (host only; no device calls).
@@ -525,9 +527,11 @@ int zero_gather_write(const float *master, int64_t shard_len, const zero_chunk *
  * squared is exact in double) in an order fixed by the element count or the
  * table, so the same call gives the same bits every time.
  *
- * Workspace: device memory, 16-byte aligned, zero_norm_workspace(n_pieces)
- * bytes (n_pieces = 0 is enough for zero_reduce_norm_shard).  Its content
- * means nothing between calls and needs no initialisation.  Calls that may
+ * Workspace: device memory, 16-byte aligned: zero_norm_workspace(n_pieces)
+ * bytes for zero_norm_pieces; zero_norm_workspace(0), 16 MiB and a little, is
+ * enough for zero_reduce_norm_shard on any shard (8 bytes for every 256
+ * elements, and 2 KiB, for a smaller one).  Its content means nothing between calls
+ * and needs no initialisation.  Calls that may
  * run at the same time (other streams, graphs replayed side by side) need a
  * workspace each.
  */

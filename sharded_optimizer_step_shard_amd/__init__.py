@@ -36,7 +36,7 @@ ZERO_SMALL_LAUNCH_CHUNKS = 2048        # 16-byte and extended steps
 ZERO_SMALL_LAUNCH_CHUNKS_12B = 16384   # 12-byte step
 ZERO_DEFAULT_MAX_CHUNK_REDUCED = 1024  # clipped steps on a reduced fp32 gradient
 ZERO_DEFAULT_MAX_PIECE = 16384         # calls over many tensors
-ZERO_NORM_PARTIALS = 16384
+ZERO_NORM_PARTIALS = 1 << 21
 ZERO_PROBE_SUM_MAX = 16
 
 # Mirrors `zero_chunk` (32 bytes).
@@ -266,7 +266,7 @@ def clip_spec(out: Ptr, max_norm: float, eps: float = 1e-6, inv_scale: float = 1
 
 def zero_norm_workspace(n_pieces: int = 0) -> int:
     """Bytes of workspace for zero_norm_pieces over n_pieces; 0 for
-    zero_reduce_norm_shard."""
+    zero_reduce_norm_shard on any shard."""
     n = _lib.zero_norm_workspace(n_pieces)
     if n < 0:
         raise ZeroShardError(ZERO_ERR_INVALID, "zero_norm_workspace")

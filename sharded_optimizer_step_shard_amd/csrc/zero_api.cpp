@@ -676,7 +676,7 @@ int64_t zero_norm_workspace(int64_t n_pieces)
 {
     if (n_pieces < 0 || n_pieces > INT32_MAX)
         return -1;
-    return 8 * (n_pieces < ZERO_NORM_PARTIALS ? (int64_t)ZERO_NORM_PARTIALS : n_pieces);
+    return 8 * (n_pieces ? n_pieces : (int64_t)ZERO_NORM_PARTIALS + 256);
 }
 
 int zero_reduce_norm_shard(const void *const *partials, int n_ranks, int gdt,
@@ -693,7 +693,8 @@ int zero_reduce_norm_shard(const void *const *partials, int n_ranks, int gdt,
     if (bad_len(n) || !sq || !workspace || workspace_bytes < 0 || (spec && !valid_clip_spec(spec)) ||
         !valid_reduce_spec(r, n_ranks))
         return ZERO_ERR_INVALID;
-    const int64_t need = zero_norm_workspace(0);
+    // an unknown type is refused below; here it counts as the wider one
+    const int64_t need = reduce_norm_workspace(n, gdt == ZERO_BF16 ? ZERO_BF16 : ZERO_FP32);
     if (workspace_bytes < need)
         return ZERO_ERR_CAPACITY;
     if (!partials_aligned(a.parts, n_ranks) || !aligned16(grad_out) || !aligned16(r->acc) ||

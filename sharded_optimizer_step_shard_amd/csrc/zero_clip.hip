@@ -50,7 +50,7 @@ __device__ __forceinline__ void write_clip(double sq, const ClipArgs &c)
 
 // The sum of part[0 .. n) by a whole workgroup of kFinishBlock lanes: lane i
 // adds part[i], part[i + kFinishBlock], ..., then the waves' sums are added in
-// order.  Returned in wave 0.
+// order.
 __device__ __forceinline__ double block_sum(const double *part, int64_t n)
 {
     __shared__ double waves[kFinishWaves];
@@ -67,6 +67,19 @@ __device__ __forceinline__ double block_sum(const double *part, int64_t n)
     for (int w = 1; w < kFinishWaves; ++w)
         t = t + waves[w];
     return t;
+}
+
+// Many partial sums become kFoldRuns first: workgroup b adds the b-th run of
+// `run` of them.
+constexpr int kFoldRuns = 256;
+
+__global__ __launch_bounds__(kFinishBlock) void norm_fold_kernel(const double *part, int64_t n, int64_t run,
+                                                                 double *out)
+{
+    const int64_t lo = blockIdx.x * run;
+    const double s = block_sum(part + lo, n - lo < run ? n - lo : run);
+    if (threadIdx.x == 0)
+        out[blockIdx.x] = s;
 }
 
 // Tensor sums: the wave that meets a tensor's first piece adds its pieces.
@@ -118,67 +131,195 @@ __global__ __launch_bounds__(kStepLanes) void clip_coef_kernel(const double *sq,
 
 // ------------------------------------------------------- reduce with the norm
 
-// The launch of the accumulate kernel: one wave a workgroup, workgroup b on
-// spans b, b + gridDim.x, ... of kNormSpan elements, and its squares in one
-// double of each lane until the end.
-constexpr int64_t kNormSpan = 2048;
+// A wave pass takes a 16-byte load of each partial a lane: 512 elements of bf16
+// (8 a lane), 256 of fp32 (4 a lane).  The reduced gradient leaves in rows of
+// 256 elements, one 16-byte store a lane, so that each store instruction
+// writes one run of 1 KiB; with bf16 partials a lane's 8 results first change
+// places through LDS (two 16-byte stores a lane, each instruction writing
+// every other 16 bytes, cost X).
+constexpr int kRow = 4 * kStepLanes;
+
+// Results e[0 .. VEC) of the group at 'lane' -> row r holds elements r * 256 +
+// 4 * lane ... of the wave's pass.
+template <int VEC>
+__device__ __forceinline__ void to_rows(f32x4 *row, const float *e, f32x4 *lds, int lane)
+{
+    if constexpr (VEC == 4) {
+        row[0] = (f32x4){e[0], e[1], e[2], e[3]};
+    } else {
+        lds[2 * lane] = (f32x4){e[0], e[1], e[2], e[3]};
+        lds[2 * lane + 1] = (f32x4){e[4], e[5], e[6], e[7]};
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        row[0] = lds[lane];
+        row[1] = lds[kStepLanes + lane];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// The two-level fold, one partial at a time: t sums a group of K in rank
+// order, s the groups in order.  KC < 0: the flat order; KC > 0: K = KC, every
+// test folding away where the ranks are unrolled; 0: K at run time.
+template <int VEC, int KC> struct Fold {
+    double s[VEC], t[VEC];
+    int K, at = 0;
+    bool some = false, begun = false;
+
+    __device__ __forceinline__ explicit Fold(int k) : K(KC > 0 ? KC : k) {}
+    __device__ __forceinline__ void close()
+    {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            s[j] = some ? s[j] + t[j] : t[j];
+        some = true;
+    }
+    template <zero_dtype G> __device__ __forceinline__ void add(u32x4 raw)
+    {
+        if constexpr (KC >= 0) {
+            if (at == K) {
+                close();
+                at = 0;
+            }
+            if (at == 0)
+                Grad<G>::first(t, raw);
+            else
+                Grad<G>::add(t, raw);
+            ++at;
+        } else {
+            if (!begun)
+                Grad<G>::first(t, raw);
+            else
+                Grad<G>::add(t, raw);
+            begun = true;
+        }
+    }
+    template <zero_dtype G, int B>
+    __device__ __forceinline__ void batch(const PartialPtrs &pp, int k, int64_t i)
+    {
+        u32x4 raw[B];
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            raw[j] = ld_raw(pp.p[k + j], i * Grad<G>::BYTES);
+        __builtin_amdgcn_sched_barrier(0);   // every load of the batch in flight
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            add<G>(raw[j]);
+    }
+};
+
+// The sum over the ranks of a lane's word at element i, in s.  NC = 0: the
+// number of ranks at run time, in batches of 8, 4, 2 and 1.
+template <zero_dtype G, int NC, int KC, int VEC>
+__device__ __forceinline__ void word_sum(double *s, const PartialPtrs &pp, int n, int K, int64_t i)
+{
+    Fold<VEC, KC> f(K);
+    if constexpr (NC > 0) {
+        constexpr int B = NC < kStepBatch ? NC : kStepBatch;
+#pragma unroll
+        for (int k = 0; k < NC; k += B)
+            f.template batch<G, B>(pp, k, i);
+    } else {
+        int k = 0;
+        for (; k + 8 <= n; k += 8)
+            f.template batch<G, 8>(pp, k, i);
+        if (n & 4) {
+            f.template batch<G, 4>(pp, k, i);
+            k += 4;
+        }
+        if (n & 2) {
+            f.template batch<G, 2>(pp, k, i);
+            k += 2;
+        }
+        if (n & 1)
+            f.template batch<G, 1>(pp, k, i);
+    }
+    f.close();
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+        s[j] = f.s[j];
+}
+
+// One element by a whole wave, lane k loading partial k (there are at most 64):
+// the loads take one round trip, the sum stays in rank order.
+template <zero_dtype G>
+__device__ __forceinline__ double wave_elem_sum(const PartialPtrs &pp, int n, int K, int64_t i)
+{
+    static_assert(ZERO_MAX_RANKS <= kStepLanes, "a lane a rank");
+    const double mine = (int)threadIdx.x < n ? Grad<G>::one(pp.p[threadIdx.x], i) : 0.0;
+    double s = 0.0, t = 0.0;
+    for (int k = 0; k < n; ++k) {
+        const double x = __shfl(mine, k);
+        if (k % K == 0) {
+            s = k == 0 ? s : (k == K ? t : s + t);
+            t = x;
+        } else {
+            t = t + x;
+        }
+    }
+    return n == K ? t : s + t;
+}
 
 // DIV: 1 multiplies by the exact reciprocal of a power of two, 2 divides.
 template <zero_dtype G, int NC, int KC, int DIV>
-__device__ __forceinline__ double reduce_norm_spans(const ReduceNormArgs &a)
+__device__ __forceinline__ double reduce_norm_passes(const ReduceNormArgs &a, f32x4 *lds)
 {
-    constexpr int VEC = Grad<G>::VEC;
-    constexpr int64_t GPS = kNormSpan / VEC;
+    constexpr int VEC = Grad<G>::VEC, ROWS = VEC / 4, PASS = VEC * kStepLanes;
     const int n = NC > 0 ? NC : a.red.n_ranks;
-    const int64_t groups = a.n / VEC;
+    const int lane = (int)threadIdx.x;
+    const int64_t whole = a.n - a.n % VEC;   // the last n % VEC elements come after
+    const int64_t first = (int64_t)blockIdx.x * a.passes * PASS;
     double sq = 0.0;
-    for (int64_t sp = blockIdx.x; sp * GPS < groups; sp += gridDim.x) {
-        const int64_t gend = (sp + 1) * GPS < groups ? (sp + 1) * GPS : groups;
-        for (int64_t g = sp * GPS + threadIdx.x; g < gend; g += kStepBlock) {
-            const int64_t i0 = g * VEC;
-            F32x<VEC> acc, out;
+    for (int64_t at = first; at < first + a.passes * PASS && at < whole; at += PASS) {
+        // past the end of the shard a lane reads its last group, and drops it
+        const bool mine = at + VEC * lane < whole;
+        const int64_t i = mine ? at + VEC * lane : whole - VEC;
+        F32x<VEC> acc;
+        if (a.acc)
+            acc.load(a.acc + i);
+        double s[VEC];
+        word_sum<G, NC, KC, VEC>(s, a.parts, n, a.red.group, i);
+        float g[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
             if (a.acc)
-                acc.load(a.acc + i0);
-            double s[VEC];
-            if constexpr (KC < 0)
-                group_sum<G, NC, kStepBatch>(s, a.parts, n, i0);
-            else
-                group_sum_two_level<G, NC, KC, kStepBatch>(s, a.parts, n, a.red.group, i0);
-            if (a.acc) {
+                s[j] = (double)acc[j] + s[j];
+            g[j] = DIV == 1 ? (float)(s[j] * a.red.inv_n) : (float)(s[j] / a.red.n);
+            sq = square_add(mine ? (double)g[j] : 0.0, sq);
+        }
+        if (a.out) {
+            f32x4 row[ROWS];
+            to_rows<VEC>(row, g, lds, lane);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    s[j] = (double)acc[j] + s[j];
+            for (int r = 0; r < ROWS; ++r) {
+                const int64_t o = at + r * kRow + 4 * lane;
+                if (o < whole)
+                    st_nt((f32x4 *)(a.out + o), row[r]);
             }
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                out[j] = DIV == 1 ? (float)(s[j] * a.red.inv_n) : (float)(s[j] / a.red.n);
-                sq = square_add((double)out[j], sq);
-            }
-            if (a.out)
-                out.store(a.out + i0);
         }
     }
-    if (blockIdx.x == 0) {
-        const int64_t i = groups * VEC + threadIdx.x;   // the last n % VEC elements
-        if (i < a.n) {
-            double e = elem_sum_two_level<G>(a.parts, n, a.red.group, i);
+    if (blockIdx.x == gridDim.x - 1) {
+        for (int64_t e = whole; e < a.n; ++e) {
+            double x = wave_elem_sum<G>(a.parts, n, a.red.group, e);
             if (a.acc)
-                e = (double)a.acc[i] + e;
-            const float f = finish_reduce<0>(e, a.red);
-            sq = square_add((double)f, sq);
-            if (a.out)
-                a.out[i] = f;
+                x = (double)a.acc[e] + x;
+            const float g = finish_reduce<0>(x, a.red);
+            if (lane == 0) {
+                sq = square_add((double)g, sq);
+                if (a.out)
+                    a.out[e] = g;
+            }
         }
     }
     return sq;
 }
 
-template <zero_dtype G, int NC, int KC>
-__global__ __launch_bounds__(kStepBlock) __attribute__((amdgpu_waves_per_eu(1, 1)))
+// W: resident waves per SIMD.
+template <zero_dtype G, int NC, int KC, int W>
+__global__ __launch_bounds__(kStepBlock) __attribute__((amdgpu_waves_per_eu(1, W)))
 void reduce_norm_kernel(ReduceNormArgs a)
 {
-    const double sq = wave_sum(a.red.pow2 ? reduce_norm_spans<G, NC, KC, 1>(a)
-                                          : reduce_norm_spans<G, NC, KC, 2>(a));
+    __shared__ f32x4 lds[2 * kStepLanes];
+    const double sq = wave_sum(a.red.pow2 ? reduce_norm_passes<G, NC, KC, 1>(a, lds)
+                                          : reduce_norm_passes<G, NC, KC, 2>(a, lds));
     if (threadIdx.x == 0)
         a.part[blockIdx.x] = sq;
 }
@@ -324,63 +465,95 @@ __global__ __launch_bounds__(kStepBlock) void norm_pieces_kernel(PiecesArgs a)
     }
 }
 
-// coef times a piece.  The stores are aligned: up to 15 bytes before dst's
-// first 16-byte boundary are done element by element, as is the end; the loads
-// go by them, at any address.
+// VEC elements (4 or 8) at any address their size divides, widened; and
+// narrowed into an address aligned for all of them.
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+
+template <int S, int VEC> struct Load {
+    static constexpr int BYTES = VEC * Elem<S>::BYTES;
+    u32x4 r;
+    __device__ __forceinline__ void get(const char *p)
+    {
+        if constexpr (BYTES == 16) {
+            r = ld_any(p);
+        } else {
+            const u32x2 h = __builtin_nontemporal_load((const u32x2_any *)p);
+            r = (u32x4){h.x, h.y, 0u, 0u};
+        }
+    }
+    __device__ __forceinline__ void widen(double *x) const
+    {
+        double y[Elem<S>::VEC];
+        Elem<S>::widen(y, r);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            x[j] = y[j];
+    }
+};
+
+template <int D, int VEC>
+__device__ __forceinline__ void put_group(char *p, const double *y)
+{
+    if constexpr (D == ZERO_FP32) {
+        static_assert(VEC == 4, "16 bytes of fp32");
+        st_nt((f32x4 *)p, (f32x4){(float)y[0], (float)y[1], (float)y[2], (float)y[3]});
+    } else {
+        uint32_t w[VEC / 2];
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j)
+            w[j] = Elem<D>::narrow(y[2 * j]) | (Elem<D>::narrow(y[2 * j + 1]) << 16);
+        if constexpr (VEC == 8)
+            st_nt((u32x4 *)p, (u32x4){w[0], w[1], w[2], w[3]});
+        else
+            st_nt((u32x2 *)p, (u32x2){w[0], w[1]});
+    }
+}
+
+// coef times a piece.  A lane's group is 8 elements where both types have 16
+// bits and 4 where one has 32, so that a wave's loads and its stores each
+// cover one run of memory (two 16-byte stores a lane for 8 fp32 elements, with
+// the other half of every 32 bytes left to the next instruction, ran at 2.7
+// TB/s against 4.8).  The stores are aligned: the elements before dst's first
+// 16-byte boundary are done one by one, as is the end; the loads go by them,
+// at any address.
 template <int S, int D>
 __device__ __forceinline__ void scale_piece(const zero_piece &c, double coef)
 {
     using ES = Elem<S>;
     using ED = Elem<D>;
-    constexpr int VEC = 8;
-    constexpr int NS = VEC / ES::VEC, ND = VEC / ED::VEC;   // 16-byte words of a group
+    constexpr int VEC = S == ZERO_FP32 || D == ZERO_FP32 ? 4 : 8;
+    constexpr int U = 8;
     const int lane = (int)threadIdx.x % kStepLanes;
     int head = (int)((16u - ((uintptr_t)c.dst & 15u)) & 15u) / ED::BYTES;
     if (head > c.len)
         head = c.len;
     const int groups = (c.len - head) / VEC;
     const int tail = head + groups * VEC;
-    const char *src = (const char *)c.src + (int64_t)head * ES::BYTES;
-    char *dst = (char *)c.dst + (int64_t)head * ED::BYTES;
+    const char *src = (const char *)c.src + head * ES::BYTES;
+    char *dst = (char *)c.dst + head * ED::BYTES;
     if (lane < head)
         ED::put(c.dst, lane, coef * ES::one(c.src, lane));
     if (tail + lane < c.len)
         ED::put(c.dst, tail + lane, coef * ES::one(c.src, tail + lane));
-    constexpr int U = 8 / NS;
     for (int g0 = 0; g0 < groups; g0 += U * kStepLanes) {
-        u32x4 r[U][NS];
+        Load<S, VEC> r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int g = g0 + u * kStepLanes + lane;
-            if (g < groups) {
-#pragma unroll
-                for (int q = 0; q < NS; ++q)
-                    r[u][q] = ld_any(src + ((int64_t)g * NS + q) * 16);
-            }
+            if (g < groups)
+                r[u].get(src + (int64_t)g * Load<S, VEC>::BYTES);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int g = g0 + u * kStepLanes + lane;
-            if (g >= groups)
-                break;
-            double x[VEC];
+            if (g < groups) {
+                double x[VEC];
+                r[u].widen(x);
 #pragma unroll
-            for (int q = 0; q < NS; ++q)
-                ES::widen(x + q * ES::VEC, r[u][q]);
-#pragma unroll
-            for (int q = 0; q < ND; ++q) {
-                u32x4 o;
-                if constexpr (D == ZERO_FP32) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = __float_as_uint((float)(coef * x[4 * q + j]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        o[j] = ED::narrow(coef * x[2 * j]) | (ED::narrow(coef * x[2 * j + 1]) << 16);
-                }
-                st_nt((u32x4 *)(dst + ((int64_t)g * ND + q) * 16), o);
+                for (int j = 0; j < VEC; ++j)
+                    x[j] = coef * x[j];
+                put_group<D, VEC>(dst + (int64_t)g * (VEC * ED::BYTES), x);
             }
         }
     }
@@ -452,6 +625,9 @@ void shard_step_clip_kernel(StepArgs a)
 
 // ------------------------------------------------------- launchers
 
+// More partial sums than this are folded before they are finished.
+constexpr int64_t kFoldFrom = 16384;
+
 hipError_t finish(const FinishArgs &f, hipStream_t s)
 {
     unsigned grid = 1;
@@ -463,20 +639,20 @@ hipError_t finish(const FinishArgs &f, hipStream_t s)
     return hipGetLastError();
 }
 
-template <zero_dtype G, int NC>
+template <zero_dtype G, int NC, int W>
 void launch_reduce_norm_n(const ReduceNormArgs &a, int K, dim3 grid, hipStream_t s)
 {
     const dim3 block(kStepBlock);
     constexpr int K8 = (NC % 8 == 0 && NC > 8) ? 8 : 0;
     constexpr int K4 = (NC % 4 == 0 && NC > 4) ? 4 : 0;
     if (K == 1 || K == a.red.n_ranks)
-        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, -1>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, -1, W>), grid, block, 0, s, a);
     else if (K8 == 8 && K == 8)
-        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, K8>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, K8, W>), grid, block, 0, s, a);
     else if (K4 == 4 && K == 4)
-        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, K4>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, K4, W>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, 0>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((reduce_norm_kernel<G, NC, 0, W>), grid, block, 0, s, a);
 }
 
 template <zero_dtype G>
@@ -484,14 +660,19 @@ hipError_t reduce_norm_dispatch(const ReduceNormArgs &a, dim3 grid, hipStream_t 
 {
     const int K = a.red.group;
     switch (a.red.n_ranks) {
-    case 1: launch_reduce_norm_n<G, 1>(a, K, grid, s); break;
-    case 2: launch_reduce_norm_n<G, 2>(a, K, grid, s); break;
-    case 4: launch_reduce_norm_n<G, 4>(a, K, grid, s); break;
-    case 8: launch_reduce_norm_n<G, 8>(a, K, grid, s); break;
-    case 16: launch_reduce_norm_n<G, 16>(a, K, grid, s); break;
-    case 32: launch_reduce_norm_n<G, 32>(a, K, grid, s); break;
-    case 64: launch_reduce_norm_n<G, 64>(a, K, grid, s); break;
-    default: launch_reduce_norm_n<G, 0>(a, K, grid, s); break;
+    case 1: launch_reduce_norm_n<G, 1, 8>(a, K, grid, s); break;
+    case 2: launch_reduce_norm_n<G, 2, 8>(a, K, grid, s); break;
+    case 4: launch_reduce_norm_n<G, 4, 4>(a, K, grid, s); break;
+    case 8: launch_reduce_norm_n<G, 8, 2>(a, K, grid, s); break;
+    case 16: launch_reduce_norm_n<G, 16, 2>(a, K, grid, s); break;
+    case 32: launch_reduce_norm_n<G, 32, 1>(a, K, grid, s); break;
+    case 64: launch_reduce_norm_n<G, 64, 1>(a, K, grid, s); break;
+    default:
+        if (a.red.n_ranks < 8)
+            launch_reduce_norm_n<G, 0, 4>(a, K, grid, s);
+        else
+            launch_reduce_norm_n<G, 0, 2>(a, K, grid, s);
+        break;
     }
     return hipGetLastError();
 }
@@ -526,21 +707,45 @@ hipError_t step_clip_layout(const StepArgs &a, zero_dtype gdt, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_reduce_norm(const ReduceNormArgs &a, zero_dtype gdt, FinishArgs f, hipStream_t s)
+hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hipStream_t s)
 {
     f.part = a.part;
-    f.n_part = 0;
-    if (a.n > 0) {
-        f.n_part = (a.n + kNormSpan - 1) / kNormSpan;
-        if (f.n_part > ZERO_NORM_PARTIALS)
-            f.n_part = ZERO_NORM_PARTIALS;
+    f.n_part = reduce_norm_waves(a.n, gdt, &a.passes);
+    if (f.n_part > 0) {
         const dim3 grid((unsigned)f.n_part);
         const hipError_t e = gdt == ZERO_BF16 ? reduce_norm_dispatch<ZERO_BF16>(a, grid, s)
                                               : reduce_norm_dispatch<ZERO_FP32>(a, grid, s);
         if (e != hipSuccess)
             return e;
     }
+    if (f.n_part > kFoldFrom) {
+        const int64_t run = (f.n_part + kFoldRuns - 1) / kFoldRuns;
+        double *out = a.part + f.n_part;
+        const int64_t runs = (f.n_part + run - 1) / run;
+        hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)runs), dim3(kFinishBlock), 0, s, f.part,
+                           f.n_part, run, out);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        f.part = out;
+        f.n_part = runs;
+    }
     return finish(f, s);
+}
+
+int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t *passes)
+{
+    const int64_t pass = kStepLanes * (gdt == ZERO_BF16 ? Grad<ZERO_BF16>::VEC : Grad<ZERO_FP32>::VEC);
+    const int64_t all = (n + pass - 1) / pass;
+    *passes = (all + ZERO_NORM_PARTIALS - 1) / ZERO_NORM_PARTIALS;
+    return all ? (all + *passes - 1) / *passes : 0;
+}
+
+int64_t reduce_norm_workspace(int64_t n, zero_dtype gdt)
+{
+    int64_t passes;
+    const int64_t waves = reduce_norm_waves(n, gdt, &passes);
+    return 8 * (waves + (waves > kFoldFrom ? kFoldRuns : 0));
 }
 
 hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s)

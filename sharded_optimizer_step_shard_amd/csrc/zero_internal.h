@@ -62,7 +62,8 @@ struct ClipArgs {
     double *out;
 };
 
-// The reduce with the norm: each workgroup leaves its sum of squares in part.
+// The reduce with the norm: each wave takes `passes` runs of one load a lane
+// and leaves its sum of squares in part.
 struct ReduceNormArgs {
     PartialPtrs parts;
     ReduceScalars red;
@@ -70,6 +71,7 @@ struct ReduceNormArgs {
     float *out;         // reduced gradient, or null
     double *part;
     int64_t n;
+    int64_t passes;     // set at launch
 };
 
 // What becomes of n_part partial sums: the total, the coefficient, and, with
@@ -134,7 +136,11 @@ hipError_t launch_reduce(const ReduceArgs &a, zero_dtype gdt, hipStream_t s);
 hipError_t launch_adamw(const AdamArgs &a, hipStream_t s);
 hipError_t launch_gather(const GatherArgs &a, hipStream_t s);
 hipError_t launch_step_clipped(const StepArgs &a, zero_dtype gdt, StateLayout layout, hipStream_t s);
-hipError_t launch_reduce_norm(const ReduceNormArgs &a, zero_dtype gdt, FinishArgs f, hipStream_t s);
+hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hipStream_t s);
+// Waves of that launch over n elements, each of *passes passes, and the bytes
+// of workspace that it uses.
+int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t *passes);
+int64_t reduce_norm_workspace(int64_t n, zero_dtype gdt);
 hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s);
 hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s);
 hipError_t launch_scale_pieces(const PiecesArgs &a, hipStream_t s);

@@ -34,8 +34,9 @@ BAD_SPECS = [dict(max_norm=-1.0), dict(max_norm=NAN), dict(eps=-1e-9), dict(eps=
 # ---------------------------------------------------------------- workspace
 
 def test_workspace_sizes():
-    assert zs.zero_norm_workspace() == 8 * zs.ZERO_NORM_PARTIALS
-    assert zs.zero_norm_workspace(zs.ZERO_NORM_PARTIALS + 1) == 8 * (zs.ZERO_NORM_PARTIALS + 1)
+    assert zs.zero_norm_workspace() >= 8 * zs.ZERO_NORM_PARTIALS
+    for n in (1, 24, zs.ZERO_NORM_PARTIALS + 1):
+        assert zs.zero_norm_workspace(n) == 8 * n
     for bad in (-1, 1 << 31):
         with pytest.raises(zs.ZeroShardError):
             zs.zero_norm_workspace(bad)
@@ -68,7 +69,12 @@ def test_reduce_norm_refusals():
     holed = parts(4)
     holed[2] = None
     assert reduce_norm(p=holed) == INVALID
-    assert reduce_norm(ws_bytes=zs.zero_norm_workspace() - 1) == CAPACITY
+    # a sum for every 512 elements of bf16, 256 of fp32, and 256 more for long shards
+    for n, gdt, need in ((1000, 0, 16), (1000, 1, 32), (512 * 16384, 0, 8 * 16384), (512 * 16385, 0, 8 * (16385 + 256)),
+                         (1 << 31, 0, 8 * ((1 << 21) + 256)), (1 << 48, 1, 8 * ((1 << 21) + 256))):
+        assert reduce_norm(n=n, gdt=gdt, out=None, p=parts(1), n_ranks=1, ws_bytes=need - 1) == CAPACITY
+        assert reduce_norm(n=n, gdt=gdt, out=None, p=parts(1), n_ranks=1, ws_bytes=need) in (NOT_DEVICE, ALIAS)
+        assert need <= zs.zero_norm_workspace()
     crooked = parts(4)
     crooked[3] = at(103) + 8
     for bad in (dict(p=crooked), dict(out=at(1) + 4), dict(sq=at(2) + 4), dict(ws=at(3) + 8),
@@ -77,8 +83,8 @@ def test_reduce_norm_refusals():
     for gdt in (2, 3, -1):                                # fp16 is for pieces alone
         assert reduce_norm(gdt=gdt) == UNSUPPORTED
     for bad in (dict(out=at(100) + 1984), dict(sq=at(100) + 8), dict(sq=at(1) + 8), dict(ws=at(1) + 16),
-                dict(ws=at(2) - 16), dict(sp=spec(out=at(2))), dict(sp=spec(out=at(101))),
-                dict(rs=rspec(0, 2, at(1) + 16)), dict(rs=rspec(0, 2, at(3) + 160)),
+                dict(ws=at(2)), dict(sp=spec(out=at(2))), dict(sp=spec(out=at(101))),
+                dict(rs=rspec(0, 2, at(1) + 16)), dict(rs=rspec(0, 2, at(3) - 16)),
                 dict(rs=rspec(0, 2, at(2) - 16))):
         assert reduce_norm(**bad) == ALIAS, bad
 

@@ -3,10 +3,9 @@ the CPU oracle.
 
 Tolerances.  A sum of squares is a sum of non-negative doubles whose terms are
 exact, so its relative error is at most k 2^-53 with k the additions any term
-passes through: here at most 128 in a lane (a piece of 16384 elements, 64
-lanes, 4 sums a lane: 64; a lane of the reduce: 32 a span and at most 4 spans
-at these sizes), 8 over the lanes and 40 in the second launch, so 176 2^-53 <
-2e-14.  The norm is its square root (half the error, and two roundings), the
+passes through: here at most 64 in a lane (a piece of 16384 elements, 64
+lanes, 4 sums a lane; a lane of the reduce: 8 a pass), 8 over the lanes and,
+joining them, at most 16 + 6 + 16 twice, so 148 2^-53 < 2e-14.  The norm is its square root (half the error, and two roundings), the
 coefficient a quotient of it (two more): 2e-14 holds for those too.  math.fsum
 rounds once.  Everything else is compared bit for bit: scaled values with the
 64-bit product rounded once, gradients and steps with the oracle, both from
@@ -133,16 +132,29 @@ def test_reduce_norm_of_an_empty_shard_is_zero(zs):
     assert sq.item() == 0.0 and clip.tolist() == [0.0, 1.0]
 
 
-def test_reduce_norm_spans_more_than_one_to_a_wave(zs):
-    """Longer than ZERO_NORM_PARTIALS spans: waves take several, and the same
-    call gives the same bits again."""
-    n = zs.ZERO_NORM_PARTIALS * 2048 + 12345
-    x = torch.empty(n, device="cuda").normal_(0, 1e-3, generator=torch.Generator("cuda").manual_seed(1))
+@pytest.mark.parametrize("gdt", ["bf16", "fp32"])
+def test_reduce_norm_in_more_than_one_pass_to_a_wave(zs, gdt):
+    """Longer than one pass for each of ZERO_NORM_PARTIALS waves: waves take two,
+    their sums are folded before they are finished, and the same call gives the
+    same bits again.  All elements but a few are one power of two, so that the
+    sum is exact in any order."""
+    kind = torch.bfloat16 if gdt == "bf16" else torch.float32
+    n = zs.ZERO_NORM_PARTIALS * (512 if gdt == "bf16" else 256) + 12345
+    x = torch.full((n,), 2.0 ** -10, dtype=kind, device="cuda")
+    for i, y in ((0, 3.0), (n // 2, 5.0), (n - 1, 7.0)):
+        x[i] = y
     sq, again, g = f64(), f64(), torch.empty(n, device="cuda")
     zs.zero_reduce_norm_shard([x], n, sq, workspace(zs), grad_out=g)
     zs.zero_reduce_norm_shard([x], n, again, workspace(zs))
-    assert torch.equal(g, x) and sq.item() == again.item()
-    near(sq.item(), math.fsum(np.square(x.cpu().numpy().astype(np.float64)).reshape(-1).tolist()), "square")
+    assert torch.equal(g, x.float()) and sq.item() == again.item() == (n - 3) * 2.0 ** -20 + 83.0
+
+
+@pytest.mark.parametrize("n", [512 * 16384, 512 * 16384 + 1, 512 * 16385 + 7])
+def test_reduce_norm_around_the_fold(zs, n):
+    x = torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(0, 1e-3, generator=torch.Generator("cuda").manual_seed(1))
+    sq = f64()
+    zs.zero_reduce_norm_shard([x], n, sq, workspace(zs))
+    near(sq.item(), math.fsum(np.square(x.double().cpu().numpy()).tolist()), "square")
 
 
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
