@@ -410,9 +410,11 @@ __device__ __forceinline__ zero_piece piece_at(const zero_piece *table, int64_t 
     return c;
 }
 
-// This lane's part of a piece's sum of squares: kPieceUnroll loads of 16
-// bytes in flight, lanes past the end adding zeros.
-constexpr int kPieceUnroll = 8;
+// This lane's part of a piece's sum of squares: kNormUnroll loads of 16 bytes
+// in flight, lanes past the end adding zeros.
+constexpr int kNormWaves = 8;
+constexpr int kNormUnroll = 1;
+constexpr int kNormBlock = kNormWaves * kStepLanes;
 
 template <int DT>
 __device__ __forceinline__ double piece_square(const zero_piece &c)
@@ -421,16 +423,19 @@ __device__ __forceinline__ double piece_square(const zero_piece &c)
     const char *src = (const char *)c.src;
     const int words = c.len / E::VEC;
     double s[4] = {0.0, 0.0, 0.0, 0.0};
-    for (int w0 = 0; w0 < words; w0 += kPieceUnroll * kStepLanes) {
-        u32x4 r[kPieceUnroll];
+    const int i = words * E::VEC + (int)threadIdx.x;
+    if (i < c.len)
+        s[0] = square_add(E::one(c.src, i), s[0]);
+    for (int w0 = 0; w0 < words; w0 += kNormUnroll * kNormBlock) {
+        u32x4 r[kNormUnroll];
 #pragma unroll
-        for (int u = 0; u < kPieceUnroll; ++u) {
-            const int w = w0 + u * kStepLanes + (int)threadIdx.x % kStepLanes;
+        for (int u = 0; u < kNormUnroll; ++u) {
+            const int w = w0 + u * kNormBlock + (int)threadIdx.x;
             r[u] = w < words ? ld_any(src + (int64_t)w * 16) : (u32x4){0u, 0u, 0u, 0u};
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < kPieceUnroll; ++u) {
+        for (int u = 0; u < kNormUnroll; ++u) {
             double x[E::VEC];
             E::widen(x, r[u]);
 #pragma unroll
@@ -438,30 +443,34 @@ __device__ __forceinline__ double piece_square(const zero_piece &c)
                 s[j % 4] = square_add(x[j], s[j % 4]);
         }
     }
-    const int i = words * E::VEC + (int)threadIdx.x % kStepLanes;
-    if (i < c.len)
-        s[0] = square_add(E::one(c.src, i), s[0]);
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-__device__ __forceinline__ double piece_sum(const zero_piece &c)
+// A workgroup a piece.
+__global__ __launch_bounds__(kNormBlock) void norm_pieces_kernel(PiecesArgs a)
 {
-    double s = 0.0;
-    if (c.src_dt == ZERO_BF16)
-        s = piece_square<ZERO_BF16>(c);
-    else if (c.src_dt == ZERO_FP32)
-        s = piece_square<ZERO_FP32>(c);
-    else if (c.src_dt == ZERO_FP16)
-        s = piece_square<ZERO_FP16>(c);
-    return wave_sum(s);
-}
-
-__global__ __launch_bounds__(kStepBlock) void norm_pieces_kernel(PiecesArgs a)
-{
-    for (int64_t p = blockIdx.x; p < a.n_pieces; p += gridDim.x) {
-        const double s = piece_sum(piece_at(a.pieces, p));
-        if (threadIdx.x == 0)
-            a.part[p] = s;
+    __shared__ double waves[2][kNormWaves];
+    int side = 0;   // two sets of sums in turn: one barrier a piece is enough
+    for (int64_t p = blockIdx.x; p < a.n_pieces; p += gridDim.x, side ^= 1) {
+        const zero_piece c = piece_at(a.pieces, p);
+        double s = 0.0;
+        if (c.src_dt == ZERO_BF16)
+            s = piece_square<ZERO_BF16>(c);
+        else if (c.src_dt == ZERO_FP32)
+            s = piece_square<ZERO_FP32>(c);
+        else if (c.src_dt == ZERO_FP16)
+            s = piece_square<ZERO_FP16>(c);
+        s = wave_sum(s);
+        if (threadIdx.x % kStepLanes == 0)
+            waves[side][threadIdx.x / kStepLanes] = s;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            double t = waves[side][0];
+#pragma unroll
+            for (int w = 1; w < kNormWaves; ++w)
+                t = t + waves[side][w];
+            a.part[p] = t;
+        }
     }
 }
 
@@ -509,82 +518,101 @@ __device__ __forceinline__ void put_group(char *p, const double *y)
     }
 }
 
-// coef times a piece.  A lane's group is 8 elements where both types have 16
-// bits and 4 where one has 32, so that a wave's loads and its stores each
-// cover one run of memory (two 16-byte stores a lane for 8 fp32 elements, with
-// the other half of every 32 bytes left to the next instruction, ran at 2.7
-// TB/s against 4.8).  The stores are aligned: the elements before dst's first
-// 16-byte boundary are done one by one, as is the end; the loads go by them,
-// at any address.
+// coef times part `part` of a piece, then the parts kParts further on: a
+// workgroup of kScaleWaves waves a part of kPartLen elements, each lane with
+// kScaleUnroll groups in flight.  A lane's group is 8 elements where both types
+// have 16 bits and 4 where one has 32, so that a wave's loads and its stores
+// each cover one run of memory.  The stores are aligned: the elements before
+// dst's first 16-byte boundary are done one by one, as is the end; the loads
+// go by them, at any address.
+constexpr int kScaleWaves = 8;
+constexpr int kScaleUnroll = 2;
+constexpr int kScaleBlock = kScaleWaves * kStepLanes;
+constexpr int kParts = 2;
+constexpr int kPartLen = 8192;
+
 template <int S, int D>
-__device__ __forceinline__ void scale_piece(const zero_piece &c, double coef)
+__device__ __forceinline__ void scale_piece(const zero_piece &c, int part, double coef)
 {
     using ES = Elem<S>;
     using ED = Elem<D>;
     constexpr int VEC = S == ZERO_FP32 || D == ZERO_FP32 ? 4 : 8;
-    constexpr int U = 8;
-    const int lane = (int)threadIdx.x % kStepLanes;
+    constexpr int U = kScaleUnroll;
+    const int lane = (int)threadIdx.x;
     int head = (int)((16u - ((uintptr_t)c.dst & 15u)) & 15u) / ED::BYTES;
     if (head > c.len)
         head = c.len;
     const int groups = (c.len - head) / VEC;
-    const int tail = head + groups * VEC;
     const char *src = (const char *)c.src + head * ES::BYTES;
     char *dst = (char *)c.dst + head * ED::BYTES;
-    if (lane < head)
-        ED::put(c.dst, lane, coef * ES::one(c.src, lane));
-    if (tail + lane < c.len)
-        ED::put(c.dst, tail + lane, coef * ES::one(c.src, tail + lane));
-    for (int g0 = 0; g0 < groups; g0 += U * kStepLanes) {
-        Load<S, VEC> r[U];
+    if (part == 0) {
+        const int tail = head + groups * VEC;
+        if (lane < head)
+            ED::put(c.dst, lane, coef * ES::one(c.src, lane));
+        if (tail + lane < c.len)
+            ED::put(c.dst, tail + lane, coef * ES::one(c.src, tail + lane));
+    }
+    constexpr int PART = kPartLen / VEC, PASS = U * kScaleBlock;
+    static_assert(PART % PASS == 0, "a part is whole passes");
+    for (int p0 = part * PART; p0 < groups; p0 += kParts * PART) {
+        for (int g0 = p0; g0 < p0 + PART && g0 < groups; g0 += PASS) {
+            Load<S, VEC> r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int g = g0 + u * kStepLanes + lane;
-            if (g < groups)
-                r[u].get(src + (int64_t)g * Load<S, VEC>::BYTES);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * kScaleBlock + lane;
+                if (g < groups)
+                    r[u].get(src + (int64_t)g * Load<S, VEC>::BYTES);
+            }
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int g = g0 + u * kStepLanes + lane;
-            if (g < groups) {
-                double x[VEC];
-                r[u].widen(x);
+            for (int u = 0; u < U; ++u) {
+                const int g = g0 + u * kScaleBlock + lane;
+                if (g < groups) {
+                    double x[VEC];
+                    r[u].widen(x);
 #pragma unroll
-                for (int j = 0; j < VEC; ++j)
-                    x[j] = coef * x[j];
-                put_group<D, VEC>(dst + (int64_t)g * (VEC * ED::BYTES), x);
+                    for (int j = 0; j < VEC; ++j)
+                        x[j] = coef * x[j];
+                    put_group<D, VEC>(dst + (int64_t)g * (VEC * ED::BYTES), x);
+                }
             }
         }
     }
 }
 
 template <int S>
-__device__ __forceinline__ void scale_to(const zero_piece &c, double coef)
+__device__ __forceinline__ void scale_to(const zero_piece &c, int part, double coef)
 {
     if (c.dst_dt == ZERO_BF16)
-        scale_piece<S, ZERO_BF16>(c, coef);
+        scale_piece<S, ZERO_BF16>(c, part, coef);
     else if (c.dst_dt == ZERO_FP32)
-        scale_piece<S, ZERO_FP32>(c, coef);
+        scale_piece<S, ZERO_FP32>(c, part, coef);
     else if (c.dst_dt == ZERO_FP16)
-        scale_piece<S, ZERO_FP16>(c, coef);
+        scale_piece<S, ZERO_FP16>(c, part, coef);
 }
 
-__global__ __launch_bounds__(kStepBlock) void scale_pieces_kernel(PiecesArgs a)
+// The parts of a run of kPieceRun pieces come one after the other, so that the
+// workgroups that short pieces leave without work lie side by side (every
+// second workgroup idle had slowed the rest of some types to half).
+constexpr int kPieceRun = 64;
+
+__global__ __launch_bounds__(kScaleBlock) void scale_pieces_kernel(PiecesArgs a)
 {
     const double coef = ((const const_f64 *)a.clip)[1];
     if (!(coef == coef))
         return;
-    for (int64_t p = blockIdx.x; p < a.n_pieces; p += gridDim.x) {
+    const int part = (int)(blockIdx.x / kPieceRun % kParts);
+    const int64_t first = (int64_t)(blockIdx.x / (kPieceRun * kParts)) * kPieceRun + blockIdx.x % kPieceRun;
+    for (int64_t p = first; p < a.n_pieces; p += gridDim.x / kParts) {
         const zero_piece c = piece_at(a.pieces, p);
         if (c.len == 0 || !c.dst || (coef == 1.0 && c.dst == c.src && c.dst_dt == c.src_dt))
             continue;
         if (c.src_dt == ZERO_BF16)
-            scale_to<ZERO_BF16>(c, coef);
+            scale_to<ZERO_BF16>(c, part, coef);
         else if (c.src_dt == ZERO_FP32)
-            scale_to<ZERO_FP32>(c, coef);
+            scale_to<ZERO_FP32>(c, part, coef);
         else if (c.src_dt == ZERO_FP16)
-            scale_to<ZERO_FP16>(c, coef);
+            scale_to<ZERO_FP16>(c, part, coef);
     }
 }
 
@@ -624,6 +652,14 @@ void shard_step_clip_kernel(StepArgs a)
 }
 
 // ------------------------------------------------------- launchers
+
+// Workgroups of `block` lanes for `want` units of work, which stride: a power of
+// two at most, and fewer than 2^32 work-items.
+unsigned block_grid(int64_t want, int block)
+{
+    const int64_t most = (int64_t(1) << 31) / block;
+    return (unsigned)(want < most ? want : most);
+}
 
 // More partial sums than this are folded before they are finished.
 constexpr int64_t kFoldFrom = 16384;
@@ -760,7 +796,7 @@ hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s)
     f.n_part = a.n_pieces;
     f.pieces = a.pieces;
     if (a.n_pieces > 0) {
-        hipLaunchKernelGGL(norm_pieces_kernel, dim3(chunk_grid(a.n_pieces)), dim3(kStepBlock), 0, s, a);
+        hipLaunchKernelGGL(norm_pieces_kernel, dim3(block_grid(a.n_pieces, kNormBlock)), dim3(kNormBlock), 0, s, a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
@@ -770,7 +806,9 @@ hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s)
 
 hipError_t launch_scale_pieces(const PiecesArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL(scale_pieces_kernel, dim3(chunk_grid(a.n_pieces)), dim3(kStepBlock), 0, s, a);
+    const int64_t runs = (a.n_pieces + kPieceRun - 1) / kPieceRun;
+    const dim3 grid(block_grid(runs * kPieceRun * kParts, kScaleBlock));
+    hipLaunchKernelGGL(scale_pieces_kernel, grid, dim3(kScaleBlock), 0, s, a);
     return hipGetLastError();
 }
 
