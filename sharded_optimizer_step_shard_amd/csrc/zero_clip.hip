@@ -326,14 +326,24 @@ void reduce_norm_kernel(ReduceNormArgs a)
 
 // ------------------------------------------------------- many tensors
 
-// A piece starts at any multiple of its element size: 16-byte loads and
-// stores at such an address, which gfx950 does in one access.
+// A piece starts at any multiple of its element size: wide loads and stores at
+// such an address, which gfx950 does in one access.
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
 
 __device__ __forceinline__ u32x4 ld_any(const void *p)
 {
     return __builtin_nontemporal_load((const u32x4_any *)p);
 }
+
+__device__ __forceinline__ u32x2 ld_any2(const void *p)
+{
+    return __builtin_nontemporal_load((const u32x2_any *)p);
+}
+
+__device__ __forceinline__ void st_any(void *p, u32x4 x) { __builtin_nontemporal_store(x, (u32x4_any *)p); }
+__device__ __forceinline__ void st_any(void *p, u32x2 x) { __builtin_nontemporal_store(x, (u32x2_any *)p); }
+
 
 __device__ __forceinline__ double half_to_double(uint32_t h)
 {
@@ -475,8 +485,7 @@ __global__ __launch_bounds__(kNormBlock) void norm_pieces_kernel(PiecesArgs a)
 }
 
 // VEC elements (4 or 8) at any address their size divides, widened; and
-// narrowed into an address aligned for all of them.
-typedef u32x2 u32x2_any __attribute__((aligned(2)));
+// narrowed into an address.
 
 template <int S, int VEC> struct Load {
     static constexpr int BYTES = VEC * Elem<S>::BYTES;
@@ -486,7 +495,7 @@ template <int S, int VEC> struct Load {
         if constexpr (BYTES == 16) {
             r = ld_any(p);
         } else {
-            const u32x2 h = __builtin_nontemporal_load((const u32x2_any *)p);
+            const u32x2 h = ld_any2(p);
             r = (u32x4){h.x, h.y, 0u, 0u};
         }
     }
@@ -505,16 +514,17 @@ __device__ __forceinline__ void put_group(char *p, const double *y)
 {
     if constexpr (D == ZERO_FP32) {
         static_assert(VEC == 4, "16 bytes of fp32");
-        st_nt((f32x4 *)p, (f32x4){(float)y[0], (float)y[1], (float)y[2], (float)y[3]});
+        st_any(p, (u32x4){__float_as_uint((float)y[0]), __float_as_uint((float)y[1]),
+                          __float_as_uint((float)y[2]), __float_as_uint((float)y[3])});
     } else {
         uint32_t w[VEC / 2];
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j)
             w[j] = Elem<D>::narrow(y[2 * j]) | (Elem<D>::narrow(y[2 * j + 1]) << 16);
         if constexpr (VEC == 8)
-            st_nt((u32x4 *)p, (u32x4){w[0], w[1], w[2], w[3]});
+            st_any(p, (u32x4){w[0], w[1], w[2], w[3]});
         else
-            st_nt((u32x2 *)p, (u32x2){w[0], w[1]});
+            st_any(p, (u32x2){w[0], w[1]});
     }
 }
 
@@ -618,15 +628,376 @@ __global__ __launch_bounds__(kScaleBlock) void scale_pieces_kernel(PiecesArgs a)
 
 // ------------------------------------------------------- the clipped steps
 
-// Resident waves per SIMD, as the steps that do not clip.
-template <int L, zero_dtype G, int NC, bool SMALL>
-constexpr int kClipWaves = L == 0 ? (SMALL ? 2 : 1)
-                                  : (L == 1 ? kM16Waves<G, NC, SMALL> : kKahanWaves);
+// The update in fewer operations, to the same bits.  The step is defined by
+// IEEE double operations, and its three divisions and its square root are
+// most of the arithmetic (84, 102 and 126 vector instructions an element on
+// the three layouts with them), enough to hold the stream back; but only
+// values rounded to fp32 or bf16 are ever stored.  So the update direction is
+// formed from the hardware's reciprocal and reciprocal square root (relative
+// error at most 2^-23 by the ISA's manual, 2^-24.2 over 2^24 values here),
+// each refined by one Newton step (Goldschmidt's form for the root): 1.5 2^-46
+// from the root and 2^-46 from the quotient, roundings of 2^-53 beside them,
+// hence within 2^-44 of the defined value.  A result is taken if everything
+// within that bound rounds alike (Ziv's test); the few elements where that is
+// open (one in 10^5 or fewer), or where a value is not finite, take the defined
+// operations.  What is stored of the moments has no divisions in it and is
+// computed as defined.  Measured, 842M elements from the reduced gradient:
+// fp32 layout 4.40 -> 4.05 ms together with the non-temporal loads below,
+// bf16 moments 3.58 -> 2.98, pure bf16 3.79 -> 3.25.
+struct Quick {
+    double klr;    // lr / bc1
+    double ibc2;   // 1 / bc2
+    double lrwd;   // lr * weight_decay
+    double rel;    // relative bound of the test
+};
 
-// L, SMALL: as the scheduled steps.  The coefficient and, for a scheduled
-// step, the constants are read when the kernel runs.
-template <int L, zero_dtype G, int NC, bool SMALL>
-__global__ __launch_bounds__(kStepBlock) __attribute__((amdgpu_waves_per_eu(1, kClipWaves<L, G, NC, SMALL>)))
+// 1 / d: within 2^-46 after one step, 2^-53 after two.
+template <int STEPS>
+__device__ __forceinline__ double quick_inverse(double d)
+{
+    double z = __builtin_amdgcn_rcp(d);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i)
+        z = __builtin_fma(__builtin_fma(-d, z, 1.0), z, z);
+    return z;
+}
+
+// Zero, or far from where products of it with fp32 values underflow.
+__device__ __forceinline__ bool ample(double x) { return x == 0.0 || __builtin_fabs(x) >= 1e-100; }
+
+// The test needs d = sqrt(vhat) + eps to have no cancellation, eps to hide what
+// quick_update adds to vhat, and errors to stay relative ones; constants that
+// do not see to that leave every element open.
+__device__ __forceinline__ Quick quick_consts(const StepScalars &k)
+{
+    Quick q;
+    q.klr = k.lr * quick_inverse<2>(k.bc1);
+    q.ibc2 = quick_inverse<2>(k.bc2);
+    q.lrwd = k.lr * k.wd;
+    const bool fit = k.eps >= 1e-30 && ample(k.lr) && ample(k.wd) && ample(k.b1);
+    q.rel = fit ? 0x1p-44 : __builtin_inf();
+    return q;
+}
+
+// lr * mhat / (sqrt(vhat) + eps) within 2^-44.  1e-300 keeps the root of a
+// zero finite; it is lost beside any square of an fp32 value.
+__device__ __forceinline__ double quick_update(double m1, double v1, const StepScalars &k, const Quick &q)
+{
+    const double x = __builtin_fma(v1, q.ibc2, 1e-300);
+    const double y = __builtin_amdgcn_rsq(x);
+    double r = x * y;
+    r = __builtin_fma(r, __builtin_fma(-r, 0.5 * y, 0.5), r);
+    return (m1 * q.klr) * quick_inverse<1>(r + k.eps);
+}
+
+// x rounded to fp32, and whether everything within e of x rounds so too (to
+// the same zero, and to a number).
+__device__ __forceinline__ float near32(double x, double e, bool &sure)
+{
+    const float lo = (float)(x - e), hi = (float)(x + e);
+    sure = sure && lo == hi && __float_as_uint(lo) == __float_as_uint(hi);
+    return lo;
+}
+
+// The same for bf16.  Rounding by way of fp32 is rounding once unless the fp32
+// value is halfway between two bf16 values.
+__device__ __forceinline__ uint32_t near16(double x, double e, bool &sure)
+{
+    const float f = near32(x, e, sure);
+    sure = sure && (__float_as_uint(f) & 0xFFFFu) != 0x8000u;
+    return to_bf16(f);
+}
+
+// double -> bf16 for a value that is as defined.  Its low word becomes one
+// sticky bit; the 20 bits of mantissa above it fit fp32, so only the second
+// rounding rounds.  (Bf16 moments and bf16 gradients meet at halfway points too
+// often to leave those open: (9 m + g) / 10 is one for a tenth of all pairs.)
+// Results below fp32's normal numbers, where fp32 would round first, are left
+// open.
+__device__ __forceinline__ uint32_t once16(double x, bool &sure)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t low = (uint32_t)u, high = (uint32_t)(u >> 32) | (low < 1u ? low : 1u);
+    const float f = (float)__builtin_bit_cast(double, (uint64_t)high << 32);
+    constexpr int kSubnormal = 0x90;   // of either sign
+    sure = sure && !__builtin_amdgcn_classf(f, kSubnormal);
+    return to_bf16(f);
+}
+
+__device__ __forceinline__ void moments(float g32, double m0, double v0, double &m1, double &v1, const StepScalars &k)
+{
+    const double g = (double)g32;
+    m1 = k.b1 * m0 + k.c1 * g;
+    v1 = k.b2 * v0 + k.c2 * (g * g);
+}
+
+// One element of each layout, as adamw_d and kahan_elem; false where the test
+// leaves it open (what was stored is then to be overwritten by those).
+__device__ __forceinline__ bool quick_fp32(float g, float &th, float &m, float &v, const StepScalars &k, const Quick &q)
+{
+    bool sure = true;
+    double m1, v1;
+    moments(g, (double)m, (double)v, m1, v1, k);
+    const double w = quick_update(m1, v1, k, q);
+    const double t = (double)th * k.dec - w;
+    th = near32(t, __builtin_fma(__builtin_fabs(w), q.rel, __builtin_fabs(t) * 0x1p-51), sure);
+    m = (float)m1;
+    v = (float)v1;
+    return sure;
+}
+
+__device__ __forceinline__ bool quick_m16(float g, float &th, uint32_t &m, uint32_t &v, const StepScalars &k,
+                                          const Quick &q)
+{
+    bool sure = true;
+    double m1, v1;
+    moments(g, bf16_to_double(m), bf16_to_double(v), m1, v1, k);
+    const double w = quick_update(m1, v1, k, q);
+    const double t = (double)th * k.dec - w;
+    th = near32(t, __builtin_fma(__builtin_fabs(w), q.rel, __builtin_fabs(t) * 0x1p-51), sure);
+    m = once16(m1, sure);
+    v = once16(v1, sure);
+    return sure;
+}
+
+__device__ __forceinline__ bool quick_kahan(float g, uint32_t &th, uint32_t &c, uint32_t &m, uint32_t &v,
+                                            const StepScalars &k, const Quick &q)
+{
+    bool sure = true;
+    double m1, v1;
+    moments(g, bf16_to_double(m), bf16_to_double(v), m1, v1, k);
+    const double w = quick_update(m1, v1, k, q);
+    const double t0 = bf16_to_double(th), decay = q.lrwd * t0;
+    const double y = bf16_to_double(c) - (w + decay);
+    const double e = __builtin_fma(__builtin_fabs(w) + __builtin_fabs(decay), q.rel, __builtin_fabs(y) * 0x1p-51);
+    const double s = t0 + y;
+    th = near16(s, __builtin_fma(__builtin_fabs(s), 0x1p-51, e), sure);
+    const double left = y - (bf16_to_double(th) - t0);
+    c = near16(left, __builtin_fma(__builtin_fabs(left), 0x1p-51, e), sure);
+    m = once16(m1, sure);
+    v = once16(v1, sure);
+    return sure;
+}
+
+// VEC values that are read once and written back: non-temporal both ways.
+template <int VEC>
+__device__ __forceinline__ void get(F32x<VEC> &x, const float *p)
+{
+#pragma unroll
+    for (int q = 0; q < VEC / 4; ++q) {
+        const f32x4 t = __builtin_nontemporal_load((const f32x4 *)p + q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x.e[4 * q + j] = t[j];
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ void get(B16x<VEC> &x, const uint16_t *p)
+{
+    Load<ZERO_BF16, VEC> r;
+    r.get((const char *)p);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+        x.e[j] = j % 2 ? r.r[j / 2] >> 16 : r.r[j / 2] & 0xFFFFu;
+}
+
+// The state of a lane's group on layout L (0: fp32 master, m, v; 1: fp32
+// master, bf16 m, v; 2: pure bf16 with compensation) and its step.
+template <int L, int VEC> struct State;
+
+template <int VEC> struct State<0, VEC> {
+    F32x<VEC> th, m, v;
+    __device__ __forceinline__ void load(const StepArgs &a, int64_t i, const uint16_t *)
+    {
+        get(th, a.master + i);
+        get(m, a.m + i);
+        get(v, a.v + i);
+    }
+    __device__ __forceinline__ bool quick(int j, float g, const StepScalars &k, const Quick &q)
+    {
+        return quick_fp32(g, th[j], m[j], v[j], k, q);
+    }
+    __device__ __forceinline__ void exact(int j, float g, const StepScalars &k) { adamw(g, th[j], m[j], v[j], k); }
+    __device__ __forceinline__ void store(const StepArgs &a, int64_t i) const
+    {
+        th.store(a.master + i);
+        m.store(a.m + i);
+        v.store(a.v + i);
+    }
+    __device__ __forceinline__ uint32_t param(int j) { return to_bf16(th[j]); }
+};
+
+template <int VEC> struct State<1, VEC> {
+    F32x<VEC> th;
+    B16x<VEC> m, v;
+    __device__ __forceinline__ void load(const StepArgs &a, int64_t i, const uint16_t *)
+    {
+        get(th, a.master + i);
+        get(m, (const uint16_t *)a.m + i);
+        get(v, (const uint16_t *)a.v + i);
+    }
+    __device__ __forceinline__ bool quick(int j, float g, const StepScalars &k, const Quick &q)
+    {
+        return quick_m16(g, th[j], m.e[j], v.e[j], k, q);
+    }
+    __device__ __forceinline__ void exact(int j, float g, const StepScalars &k)
+    {
+        double m1, v1;
+        adamw_d(g, th[j], bf16_to_double(m.e[j]), bf16_to_double(v.e[j]), m1, v1, k);
+        m.e[j] = bf16_from_double(m1);
+        v.e[j] = bf16_from_double(v1);
+    }
+    __device__ __forceinline__ void store(const StepArgs &a, int64_t i) const
+    {
+        th.store(a.master + i);
+        m.store((uint16_t *)a.m + i);
+        v.store((uint16_t *)a.v + i);
+    }
+    __device__ __forceinline__ uint32_t param(int j) { return to_bf16(th[j]); }
+};
+
+template <int VEC> struct State<2, VEC> {
+    B16x<VEC> th, c, m, v;
+    __device__ __forceinline__ void load(const StepArgs &a, int64_t i, const uint16_t *d)
+    {
+        get(th, d);
+        get(c, a.comp + i);
+        get(m, (const uint16_t *)a.m + i);
+        get(v, (const uint16_t *)a.v + i);
+    }
+    __device__ __forceinline__ bool quick(int j, float g, const StepScalars &k, const Quick &q)
+    {
+        return quick_kahan(g, th.e[j], c.e[j], m.e[j], v.e[j], k, q);
+    }
+    __device__ __forceinline__ void exact(int j, float g, const StepScalars &k)
+    {
+        kahan_elem(g, th.e[j], c.e[j], m.e[j], v.e[j], k);
+    }
+    __device__ __forceinline__ void store(const StepArgs &a, int64_t i) const
+    {
+        c.store(a.comp + i);
+        m.store((uint16_t *)a.m + i);
+        v.store((uint16_t *)a.v + i);
+    }
+    __device__ __forceinline__ uint32_t param(int j) { return th.e[j]; }
+};
+
+// One element at a time, for the ends of a chunk that lies off the group grid.
+template <int L>
+__device__ __forceinline__ void step_one(const StepArgs &a, int64_t i, uint16_t *d, float g, const StepScalars &k)
+{
+    uint16_t *const m16 = (uint16_t *)a.m, *const v16 = (uint16_t *)a.v;
+    if constexpr (L == 0) {
+        float th = a.master[i], m = a.m[i], v = a.v[i];
+        adamw(g, th, m, v, k);
+        a.master[i] = th;
+        a.m[i] = m;
+        a.v[i] = v;
+        *d = (uint16_t)to_bf16(th);
+    } else if constexpr (L == 1) {
+        float th = a.master[i];
+        double m1, v1;
+        adamw_d(g, th, bf16_to_double(m16[i]), bf16_to_double(v16[i]), m1, v1, k);
+        a.master[i] = th;
+        m16[i] = (uint16_t)bf16_from_double(m1);
+        v16[i] = (uint16_t)bf16_from_double(v1);
+        *d = (uint16_t)to_bf16(th);
+    } else {
+        uint32_t th = *d, c = a.comp[i], m = m16[i], v = v16[i];
+        kahan_elem(g, th, c, m, v, k);
+        *d = (uint16_t)th;
+        a.comp[i] = (uint16_t)c;
+        m16[i] = (uint16_t)m;
+        v16[i] = (uint16_t)v;
+    }
+}
+
+// Two waves a chunk: with the chunks of 1024 elements that the header names for
+// a reduced gradient, two passes each (842M elements, fp32 layout: 4.03 ms;
+// one wave 4.15, four 4.30; two waves on chunks of 512 4.49, of 2048 4.34).
+// Non-temporal loads of the state, which is read once and written back
+// non-temporally: 4.31 -> 4.05 ms.
+constexpr int kClipStepWaves = 2;
+constexpr int kClipStepBlock = kClipStepWaves * kStepLanes;
+
+// One chunk by a workgroup: the gradient is an fp32 tensor before and after
+// the coefficient, as the reduced gradient it is made from.
+template <int L, zero_dtype G, int NC>
+__device__ __forceinline__ void clip_chunk(const StepArgs &a, const zero_chunk &c, const StepScalars &k,
+                                           const Quick &q, double coef)
+{
+    constexpr bool ONE = G == ZERO_FP32 && NC == 1;   // its mean is itself
+    constexpr int VEC = Grad<G>::VEC;
+    if (c.len <= 0 || c.shard_off < 0 || c.shard_off > a.shard_len - c.len)
+        return;
+    const int n = NC > 0 ? NC : a.red.n_ranks;
+    const int64_t lo = c.shard_off, hi = c.shard_off + c.len;
+    const int64_t g0 = lo / VEC, g1 = (hi + VEC - 1) / VEC;
+    for (int64_t gi = g0 + threadIdx.x; gi < g1; gi += kClipStepBlock) {
+        const int64_t i0 = gi * VEC;
+        uint16_t *d = c.dst + (i0 - lo);
+        if (i0 >= lo && i0 + VEC <= hi) {
+            State<L, VEC> st;
+            st.load(a, i0, d);
+            F32x<VEC> mean;
+            if constexpr (ONE) {
+                get(mean, (const float *)a.parts.p[0] + i0);
+            } else {
+                double s[VEC];
+                group_sum<G, NC, kStepBatch>(s, a.parts, n, i0);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    mean[j] = finish_reduce<NC>(s[j], a.red);
+            }
+            float g[VEC];
+            bool sure = true;
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+                g[j] = (float)((double)mean[j] * coef);
+                sure = st.quick(j, g[j], k, q) && sure;
+            }
+            if (__builtin_expect(!sure, 0)) {
+                st.load(a, i0, d);   // nothing has been stored yet
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    st.exact(j, g[j], k);
+            }
+            st.store(a, i0);
+            uint32_t w[VEC / 2];
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j)
+                w[j] = st.param(2 * j) | (st.param(2 * j + 1) << 16);
+            if constexpr (VEC == 8)
+                st_any(d, (u32x4){w[0], w[1], w[2], w[3]});
+            else
+                st_any(d, (u32x2){w[0], w[1]});
+        } else {
+            for (int j = 0; j < VEC; ++j) {
+                const int64_t i = i0 + j;
+                if (i >= lo && i < hi) {
+                    const float g = finish_reduce<NC>(elem_sum<G>(a.parts, n, i), a.red);
+                    step_one<L>(a, i, d + j, (float)((double)g * coef), k);
+                }
+            }
+        }
+    }
+}
+
+// Resident waves per SIMD: the more arithmetic a layout has and the fewer loads
+// a lane has in flight, the more of them.  100M elements, one to four waves:
+// fp32 layout from 8 bf16 partials 875 / 742 / 742 / 741 us, 8 fp32 957 / 965 /
+// 997 / 1011; bf16 moments 726 / 578 / 570 / 571 and 1032 / 790 / 836 / 856; pure
+// bf16 864 / 590 / 545 / 546 and 1140 / 790 / 803 / 831; from one fp32 partial
+// (842M elements) 2 to 4 waves: 4026 / 4156 / 4295, 3371 / 2976 / 2990 and
+// 3915 / 3423 / 3291.
+template <int L, zero_dtype G, int NC>
+constexpr int kClipWaves = L == 0 ? 2 : (NC * Grad<G>::BYTES > 16 ? 1 : 2) + L;
+
+// The coefficient and, for a scheduled step, the constants are read when the
+// kernel runs.
+template <int L, zero_dtype G, int NC>
+__global__ __launch_bounds__(kClipStepBlock) __attribute__((amdgpu_waves_per_eu(1, kClipWaves<L, G, NC>)))
 void shard_step_clip_kernel(StepArgs a)
 {
     const double coef = ((const const_f64 *)a.clip)[1];
@@ -641,14 +1012,9 @@ void shard_step_clip_kernel(StepArgs a)
         k.b1 = e[0]; k.c1 = e[1]; k.b2 = e[2]; k.c2 = e[3]; k.bc1 = e[4]; k.bc2 = e[5];
         k.eps = e[6]; k.lr = e[7]; k.dec = e[8]; k.wd = e[9];
     }
-    for (int64_t ci = blockIdx.x; ci < a.n_chunks; ci += gridDim.x) {
-        if constexpr (L == 0)
-            step_chunk<G, NC, false, -1, 0, true>(a, chunk_at(a.chunks, ci), k, coef);
-        else if constexpr (L == 1)
-            step_chunk_m16<G, NC, SMALL, true>(a, chunk_at(a.chunks, ci), k, coef);
-        else
-            step_chunk_kahan<G, NC, true>(a, chunk_at(a.chunks, ci), k, coef);
-    }
+    const Quick q = quick_consts(k);
+    for (int64_t ci = blockIdx.x; ci < a.n_chunks; ci += gridDim.x)
+        clip_chunk<L, G, NC>(a, chunk_at(a.chunks, ci), k, q, coef);
 }
 
 // ------------------------------------------------------- launchers
@@ -713,19 +1079,19 @@ hipError_t reduce_norm_dispatch(const ReduceNormArgs &a, dim3 grid, hipStream_t 
     return hipGetLastError();
 }
 
-template <int L, zero_dtype G, bool SMALL>
+template <int L, zero_dtype G>
 hipError_t step_clip_dispatch(const StepArgs &a, hipStream_t s)
 {
-    const dim3 grid(chunk_grid(a.n_chunks)), block(kStepBlock);
+    const dim3 grid(block_grid(a.n_chunks, kClipStepBlock)), block(kClipStepBlock);
     switch (a.red.n_ranks) {
-    case 1: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 1, SMALL>), grid, block, 0, s, a); break;
-    case 2: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 2, SMALL>), grid, block, 0, s, a); break;
-    case 4: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 4, SMALL>), grid, block, 0, s, a); break;
-    case 8: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 8, SMALL>), grid, block, 0, s, a); break;
-    case 16: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 16, SMALL>), grid, block, 0, s, a); break;
-    case 32: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 32, SMALL>), grid, block, 0, s, a); break;
-    case 64: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 64, SMALL>), grid, block, 0, s, a); break;
-    default: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 0, SMALL>), grid, block, 0, s, a); break;
+    case 1: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 1>), grid, block, 0, s, a); break;
+    case 2: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 2>), grid, block, 0, s, a); break;
+    case 4: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 4>), grid, block, 0, s, a); break;
+    case 8: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 8>), grid, block, 0, s, a); break;
+    case 16: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 16>), grid, block, 0, s, a); break;
+    case 32: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 32>), grid, block, 0, s, a); break;
+    case 64: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 64>), grid, block, 0, s, a); break;
+    default: hipLaunchKernelGGL((shard_step_clip_kernel<L, G, 0>), grid, block, 0, s, a); break;
     }
     return hipGetLastError();
 }
@@ -733,12 +1099,7 @@ hipError_t step_clip_dispatch(const StepArgs &a, hipStream_t s)
 template <int L>
 hipError_t step_clip_layout(const StepArgs &a, zero_dtype gdt, hipStream_t s)
 {
-    const bool small = a.n_chunks <= (L == 1 ? ZERO_SMALL_LAUNCH_CHUNKS_12B : ZERO_SMALL_LAUNCH_CHUNKS);
-    if (gdt == ZERO_BF16)
-        return small ? step_clip_dispatch<L, ZERO_BF16, true>(a, s)
-                     : step_clip_dispatch<L, ZERO_BF16, false>(a, s);
-    return small ? step_clip_dispatch<L, ZERO_FP32, true>(a, s)
-                 : step_clip_dispatch<L, ZERO_FP32, false>(a, s);
+    return gdt == ZERO_BF16 ? step_clip_dispatch<L, ZERO_BF16>(a, s) : step_clip_dispatch<L, ZERO_FP32>(a, s);
 }
 
 }  // namespace

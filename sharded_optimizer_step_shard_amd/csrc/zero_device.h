@@ -100,18 +100,6 @@ __device__ __forceinline__ uint32_t bf16_from_double(double d)
 
 __device__ __forceinline__ double bf16_to_double(uint32_t h) { return (double)__uint_as_float(h << 16); }
 
-// The clipped gradient is an fp32 tensor, like the reduced gradient it is made
-// from: one product in double, rounded once.  CLIP = false (the steps that do
-// not clip) passes g through.
-template <bool CLIP>
-__device__ __forceinline__ float clipped(float g, double coef)
-{
-    if constexpr (CLIP)
-        return (float)((double)g * coef);
-    else
-        return g;
-}
-
 // One element of the pure-bf16 step: AdamW's increment -lr (u + wd theta)
 // added to the bf16 parameter by Kahan's compensated summation, the bf16
 // compensation c holding the part theta has not absorbed yet:
@@ -532,10 +520,9 @@ constexpr int kStepBatch = 8;
 // DIV (extended step only): 1 when that divisor is a power of two (multiply
 // by its exact reciprocal), 2 otherwise (divide); 0 leaves the choice to
 // finish_reduce.
-// CLIP: the reduced gradient is multiplied by coef (clipped).
-template <zero_dtype G, int NC, bool EXT, int KC, int DIV = 0, bool CLIP = false>
+template <zero_dtype G, int NC, bool EXT, int KC, int DIV = 0>
 __device__ __forceinline__ void step_chunk(const StepArgs &a, const zero_chunk &c,
-                                           const StepScalars &k, double coef = 1.0)
+                                           const StepScalars &k)
 {
     constexpr int VEC = Grad<G>::VEC;
     if (c.len <= 0 || c.shard_off < 0 || c.shard_off > a.shard_len - c.len)
@@ -582,7 +569,7 @@ __device__ __forceinline__ void step_chunk(const StepArgs &a, const zero_chunk &
                     gj = (float)(s[j] / a.red.n);
                 else
                     gj = finish_reduce<EXT ? 0 : NC>(s[j], a.red);
-                adamw(clipped<CLIP>(gj, coef), th[j], m[j], v[j], k);
+                adamw(gj, th[j], m[j], v[j], k);
                 h[j] = to_bf16(th[j]);
             }
             th.store(a.master + i0);
@@ -604,7 +591,7 @@ __device__ __forceinline__ void step_chunk(const StepArgs &a, const zero_chunk &
                     gj = finish_reduce<NC>(elem_sum<G>(a.parts, n, i), a.red);
                 }
                 float th = a.master[i], m = a.m[i], v = a.v[i];
-                adamw(clipped<CLIP>(gj, coef), th, m, v, k);
+                adamw(gj, th, m, v, k);
                 a.master[i] = th;
                 a.m[i] = m;
                 a.v[i] = v;
@@ -650,9 +637,9 @@ constexpr int kM16Batch = kM16Waves<G, NC, SMALL> == 2 ? 2
 // The step on the 12-byte state: fp32 master, bf16 m and v (in a.m, a.v
 // as 16-bit patterns).  Same reduce and AdamW; the moments are read from
 // bf16 and rounded back to bf16 once, from double.
-template <zero_dtype G, int NC, bool SMALL, bool CLIP = false>
+template <zero_dtype G, int NC, bool SMALL>
 __device__ __forceinline__ void step_chunk_m16(const StepArgs &a, const zero_chunk &c,
-                                               const StepScalars &k, double coef = 1.0)
+                                               const StepScalars &k)
 {
     constexpr int VEC = Grad<G>::VEC;
     if (c.len <= 0 || c.shard_off < 0 || c.shard_off > a.shard_len - c.len)
@@ -678,8 +665,8 @@ __device__ __forceinline__ void step_chunk_m16(const StepArgs &a, const zero_chu
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 double m1, v1;
-                adamw_d(clipped<CLIP>(finish_reduce<NC>(s[j], a.red), coef), th[j],
-                        bf16_to_double(m.e[j]), bf16_to_double(v.e[j]), m1, v1, k);
+                adamw_d(finish_reduce<NC>(s[j], a.red), th[j], bf16_to_double(m.e[j]),
+                        bf16_to_double(v.e[j]), m1, v1, k);
                 m.e[j] = bf16_from_double(m1);
                 v.e[j] = bf16_from_double(v1);
                 h[j] = to_bf16(th[j]);
@@ -695,7 +682,7 @@ __device__ __forceinline__ void step_chunk_m16(const StepArgs &a, const zero_chu
                     continue;
                 float th = a.master[i];
                 double m1, v1;
-                adamw_d(clipped<CLIP>(finish_reduce<NC>(elem_sum<G>(a.parts, n, i), a.red), coef), th,
+                adamw_d(finish_reduce<NC>(elem_sum<G>(a.parts, n, i), a.red), th,
                         bf16_to_double(m16[i]), bf16_to_double(v16[i]), m1, v1, k);
                 a.master[i] = th;
                 m16[i] = (uint16_t)bf16_from_double(m1);
@@ -709,9 +696,9 @@ __device__ __forceinline__ void step_chunk_m16(const StepArgs &a, const zero_chu
 // The pure-bf16 step: the parameters are read from and written back to
 // the chunk's destination (the bf16 parameter is the only copy of the
 // weight), with bf16 compensation, m and v in shard order.
-template <zero_dtype G, int NC, bool CLIP = false>
+template <zero_dtype G, int NC>
 __device__ __forceinline__ void step_chunk_kahan(const StepArgs &a, const zero_chunk &c,
-                                                 const StepScalars &k, double coef = 1.0)
+                                                 const StepScalars &k)
 {
     constexpr int VEC = Grad<G>::VEC;
     if (c.len <= 0 || c.shard_off < 0 || c.shard_off > a.shard_len - c.len)
@@ -740,8 +727,7 @@ __device__ __forceinline__ void step_chunk_kahan(const StepArgs &a, const zero_c
             group_sum<G, NC>(s, a.parts, n, i0);
 #pragma unroll
             for (int j = 0; j < VEC; ++j)
-                kahan_elem(clipped<CLIP>(finish_reduce<NC>(s[j], a.red), coef), th.e[j], cm.e[j],
-                           m.e[j], v.e[j], k);
+                kahan_elem(finish_reduce<NC>(s[j], a.red), th.e[j], cm.e[j], m.e[j], v.e[j], k);
             cm.store(c16 + i0);
             m.store(m16 + i0);
             v.store(v16 + i0);
@@ -752,8 +738,7 @@ __device__ __forceinline__ void step_chunk_kahan(const StepArgs &a, const zero_c
                 if (i < lo || i >= hi)
                     continue;
                 uint32_t th = d[j], cm = c16[i], m = m16[i], v = v16[i];
-                kahan_elem(clipped<CLIP>(finish_reduce<NC>(elem_sum<G>(a.parts, n, i), a.red), coef), th,
-                           cm, m, v, k);
+                kahan_elem(finish_reduce<NC>(elem_sum<G>(a.parts, n, i), a.red), th, cm, m, v, k);
                 d[j] = (uint16_t)th;
                 c16[i] = (uint16_t)cm;
                 m16[i] = (uint16_t)m;

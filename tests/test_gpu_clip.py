@@ -609,3 +609,70 @@ def test_clipping_many_tensors_on_a_stream_of_its_own(zs):
     near(clip[1].item(), coef, "coef")
     for t, w, k in zip(ts, want, ("bf16", "fp32", "fp16", "bf16")):
         same_bits(t_bits(t), rounded(clip[1].item() * w, k), k)
+
+
+def awkward(rng, n, kind):
+    """Values where a shorter way to a rounding could go wrong: zeros of both
+    signs, subnormals, powers of two and their neighbours, halfway points of
+    bf16, the largest, infinities and NaN."""
+    pick = np.array([0.0, -0.0, 1e-45, -1e-45, 1e-39, 2.0 ** -126, 2.0 ** -133, 1.0, 1.0 + 2 ** -8, 1.0 + 3 * 2 ** -8, 2.0 ** -9 * 3,
+                     1 - 2 ** -9, 0.02, 3.0e38, -3.0e38, 1e-20, 1e-30], dtype=np.float32)
+    x = np.where(rng.random(n) < 0.5, pick[rng.integers(0, len(pick), n)], (rng.standard_normal(n) * 10.0 ** rng.integers(-30, 3, n)).astype(np.float32))
+    x = x.astype(np.float32)
+    x[rng.integers(0, n, 40)] = np.inf
+    x[rng.integers(0, n, 40)] = np.nan
+    return oracle.bf16_round(x) if kind == "bf16" else x
+
+
+@pytest.mark.parametrize("hp", [dict(), dict(eps=0.0), dict(eps=-1e-9), dict(eps=1e-20), dict(lr=0.0), dict(lr=-1e-3), dict(weight_decay=0.0),
+                                dict(beta1=0.0, beta2=0.0), dict(beta1=1e-300, beta2=1e-200), dict(lr=1e300), dict(lr=1e-300), dict(weight_decay=1e-300),
+                                dict(beta2=1 - 2.0 ** -53)])
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_clipped_step_on_awkward_values(zs, layout, hp):
+    """The kernels reach the defined bits by a shorter way where they can; here
+    the state, the gradient and the constants are where it is hardest."""
+    say(f"case: awkward {layout} {hp}")
+    n = 40000
+    rng = np.random.default_rng(14)
+    kinds = ["bf16"] * 3 if layout == "kahan" else ["fp32"] + ["bf16" if layout == "bf16m" else "fp32"] * 2
+    st = [awkward(rng, n, k) for k in kinds]
+    keep = rng.random(n) < 0.7               # a second moment is not negative, mostly
+    st[2] = np.where(keep, st[2] & 0x7FFF, st[2]).astype(np.uint16) if st[2].dtype == np.uint16 else np.where(keep, np.abs(st[2]), st[2])
+    prm = awkward(rng, n, "bf16")
+    args = dict(HP, **hp)
+    for kind in ("fp32", "bf16"):
+        g = awkward(rng, n, kind)
+        for coef, t in ((1.0, 1), (0.37, 1000)):
+            s = Shard(zs, layout, n, 1)
+            for d, x in zip(s.d, st):
+                d.copy_(dev(x))
+            s.slot[1:1 + n] = dev(prm)
+            getattr(zs, NAMES[layout] + "_clipped")([dev(g)], *s.d, n, s.chunks, s.n_chunks, zs.hparams(t, **args),
+                                                    torch.tensor([0.0, coef], dtype=torch.float64, device="cuda"), gdt=0 if kind == "bf16" else 1)
+            with np.errstate(over="ignore", invalid="ignore"):
+                gc = (wide(g) * coef).astype(np.float32)
+            o = oracle.hparams(t, **args)
+            if layout == "kahan":
+                th, *want = oracle.shard_step_kahan([gc], prm, *st, o)
+            else:
+                f = oracle.shard_step if layout == "fp32" else oracle.shard_step_bf16m
+                *want, th = f([gc], *st, o)
+            s.check(want, th, f"{kind} coef {coef} t {t}")
+
+
+@pytest.mark.parametrize("layout", sorted(NAMES))
+def test_many_clipped_steps_in_a_row(zs, layout):
+    """Two million elements for six steps: enough for the elements that the
+    shorter way leaves open to be among them, on every layout."""
+    n = 1 << 21
+    rng = np.random.default_rng(15)
+    s = Shard(zs, layout, n)
+    st, prm = [x.copy() for x in s.st], s.prm.copy()
+    for t in range(1, 7):
+        g = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+        if t % 2:
+            g = (oracle.bf16_round(g).astype(np.uint32) << 16).view(np.float32)
+        coef = 1.0 if t < 3 else 0.3 + 0.1 * t
+        s.step([dev(g)], torch.tensor([0.0, coef], dtype=torch.float64, device="cuda"), t=t)
+        st, prm = oracle_step(layout, (g.astype(np.float64) * coef).astype(np.float32), st, prm, t)
+        s.check(st, prm, f"step {t}")
