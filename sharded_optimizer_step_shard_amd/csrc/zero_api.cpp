@@ -676,7 +676,7 @@ int64_t zero_norm_workspace(int64_t n_pieces)
 {
     if (n_pieces < 0 || n_pieces > INT32_MAX)
         return -1;
-    return 8 * (n_pieces ? n_pieces : (int64_t)ZERO_NORM_PARTIALS + 256);
+    return n_pieces ? norm_pieces_workspace(n_pieces) : reduce_norm_workspace(ZERO_MAX_LEN, ZERO_FP32);
 }
 
 int zero_reduce_norm_shard(const void *const *partials, int n_ranks, int gdt,
@@ -753,7 +753,7 @@ int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, d
         n_tensors > INT32_MAX || !sq || !workspace || workspace_bytes < 0 ||
         (spec && !valid_clip_spec(spec)))
         return ZERO_ERR_INVALID;
-    const int64_t need = zero_norm_workspace(n_pieces);
+    const int64_t need = norm_pieces_workspace(n_pieces);
     if (workspace_bytes < need)
         return ZERO_ERR_CAPACITY;
     if (!aligned16(d_pieces) || !aligned16(workspace) || ((uintptr_t)sq & 7u) != 0 ||

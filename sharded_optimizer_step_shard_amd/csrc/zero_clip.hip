@@ -69,46 +69,88 @@ __device__ __forceinline__ double block_sum(const double *part, int64_t n)
     return t;
 }
 
-// Many partial sums become kFoldRuns first: workgroup b adds the b-th run of
-// `run` of them.
-constexpr int kFoldRuns = 256;
+// Tensor sums, by the workgroup whose kTensorRun pieces hold the tensor's first
+// one: up to kLanePieces of them by one lane, more by a wave, more than
+// kWavePieces by the workgroup.
+constexpr int kTensorRun = 256;
+constexpr int kLanePieces = 8;
+constexpr int kWavePieces = 1024;
 
-__global__ __launch_bounds__(kFinishBlock) void norm_fold_kernel(const double *part, int64_t n, int64_t run,
-                                                                 double *out)
+__device__ __forceinline__ void tensor_sums(const FinishArgs &a, int64_t run)
 {
-    const int64_t lo = blockIdx.x * run;
-    const double s = block_sum(part + lo, n - lo < run ? n - lo : run);
-    if (threadIdx.x == 0)
-        out[blockIdx.x] = s;
-}
-
-// Tensor sums: the wave that meets a tensor's first piece adds its pieces.
-__device__ __forceinline__ void tensor_sums(const FinishArgs &a, int64_t wave, int64_t n_waves)
-{
+    __shared__ int listed, first[kTensorRun], ids[kTensorRun], counts[kTensorRun];
     const int lane = threadIdx.x % kStepLanes;
-    for (int64_t p = wave; p < a.n_part; p += n_waves) {
+    if (threadIdx.x == 0)
+        listed = 0;
+    __syncthreads();
+    const int64_t lo = run * kTensorRun, p = lo + threadIdx.x;
+    if (threadIdx.x < kTensorRun && p < a.n_pieces) {
+        const int id = a.pieces[p].tensor_id;
         int64_t count = a.pieces[p].tensor_pieces;
-        const int64_t id = a.pieces[p].tensor_id;
-        if (count <= 0 || id < 0 || id >= a.n_tensors)
+        if (count > a.n_pieces - p)
+            count = a.n_pieces - p;
+        if (count > 0 && id >= 0 && id < a.n_tensors) {
+            if (count > kLanePieces) {
+                const int k = atomicAdd(&listed, 1);
+                first[k] = threadIdx.x;
+                ids[k] = id;
+                counts[k] = (int)count;
+            } else {
+                double x[kLanePieces];
+#pragma unroll
+                for (int i = 0; i < kLanePieces; ++i)
+                    x[i] = a.pieces_sq[i < count ? p + i : p];
+                double s = x[0];
+#pragma unroll
+                for (int i = 1; i < kLanePieces; ++i)
+                    s = i < count ? s + x[i] : s;
+                a.tensor_sq[id] = s;
+            }
+        }
+    }
+    __syncthreads();
+    for (int k = threadIdx.x / kStepLanes; k < listed; k += kFinishWaves) {
+        if (counts[k] > kWavePieces)
             continue;
-        if (count > a.n_part - p)
-            count = a.n_part - p;
+        const double *x = a.pieces_sq + lo + first[k];
         double s = 0.0;
-        for (int64_t i = lane; i < count; i += kStepLanes)
-            s = s + a.part[p + i];
+#pragma unroll 8
+        for (int i = lane; i < counts[k]; i += kStepLanes)
+            s = s + x[i];
         s = wave_sum(s);
         if (lane == 0)
-            a.tensor_sq[id] = s;
+            a.tensor_sq[ids[k]] = s;
+    }
+    for (int k = 0; k < listed; ++k) {
+        if (counts[k] <= kWavePieces)
+            continue;
+        const double s = block_sum(a.pieces_sq + lo + first[k], counts[k]);
+        if (threadIdx.x == 0)
+            a.tensor_sq[ids[k]] = s;
+        __syncthreads();   // before block_sum's sums are written again
     }
 }
 
+// Many partial sums become kFoldRuns first: workgroup b < f.folds adds the b-th
+// run of f.run of them; the others make the tensors' sums, if any are wanted.
+__global__ __launch_bounds__(kFinishBlock) void norm_fold_kernel(FinishArgs f)
+{
+    if (blockIdx.x >= f.folds) {
+        tensor_sums(f, blockIdx.x - f.folds);
+        return;
+    }
+    const int64_t lo = blockIdx.x * f.run;
+    const double s = block_sum(f.part + lo, f.n_part - lo < f.run ? f.n_part - lo : f.run);
+    if (threadIdx.x == 0)
+        f.folded[blockIdx.x] = s;
+}
+
 // Workgroup 0 makes the total and the coefficient; the others, launched where
-// they are asked for, the tensors' sums.
+// nothing was folded, the tensors' sums.
 __global__ __launch_bounds__(kFinishBlock) void norm_finish_kernel(FinishArgs a)
 {
     if (blockIdx.x > 0) {
-        tensor_sums(a, (int64_t)(blockIdx.x - 1) * kFinishWaves + threadIdx.x / kStepLanes,
-                    (int64_t)(gridDim.x - 1) * kFinishWaves);
+        tensor_sums(a, blockIdx.x - 1);
         return;
     }
     const double s = block_sum(a.part, a.n_part);
@@ -990,9 +1032,11 @@ __device__ __forceinline__ void clip_chunk(const StepArgs &a, const zero_chunk &
 // 997 / 1011; bf16 moments 726 / 578 / 570 / 571 and 1032 / 790 / 836 / 856; pure
 // bf16 864 / 590 / 545 / 546 and 1140 / 790 / 803 / 831; from one fp32 partial
 // (842M elements) 2 to 4 waves: 4026 / 4156 / 4295, 3371 / 2976 / 2990 and
-// 3915 / 3423 / 3291.
+// 3915 / 3423 / 3291, pure bf16 with 8: 3069.
 template <int L, zero_dtype G, int NC>
-constexpr int kClipWaves = L == 0 ? 2 : (NC * Grad<G>::BYTES > 16 ? 1 : 2) + L;
+constexpr int kClipWaves = L == 0 ? 2
+                           : L == 2 && G == ZERO_FP32 && NC == 1 ? 8
+                                                                 : (NC * Grad<G>::BYTES > 16 ? 1 : 2) + L;
 
 // The coefficient and, for a scheduled step, the constants are read when the
 // kernel runs.
@@ -1027,17 +1071,32 @@ unsigned block_grid(int64_t want, int block)
     return (unsigned)(want < most ? want : most);
 }
 
-// More partial sums than this are folded before they are finished.
+// More partial sums than kFoldFrom become kFoldRuns in a launch of their own
+// before they are finished: a call over 32226 sums took 19.0 us against 20.7
+// with one launch less, over 16406 12.9 against 12.1, over 128906 54 against 61.
 constexpr int64_t kFoldFrom = 16384;
+constexpr int kFoldRuns = 256;
 
-hipError_t finish(const FinishArgs &f, hipStream_t s)
+int64_t fold_room(int64_t n_part) { return n_part > kFoldFrom ? kFoldRuns : 0; }
+
+// f.part and f.n_part are set, f.pieces_sq and f.n_pieces where tensors' sums
+// are wanted; the workspace has room for fold_room(n_part) sums after part's.
+hipError_t finish(FinishArgs f, hipStream_t s)
 {
-    unsigned grid = 1;
-    if (f.tensor_sq && f.n_part > 0) {
-        const int64_t want = (f.n_part + kFinishWaves - 1) / kFinishWaves;
-        grid += (unsigned)(want < 1024 ? want : 1024);
+    unsigned tensors = f.tensor_sq ? (unsigned)((f.n_pieces + kTensorRun - 1) / kTensorRun) : 0;
+    if (f.n_part > kFoldFrom) {
+        f.run = (f.n_part + kFoldRuns - 1) / kFoldRuns;
+        f.folds = (unsigned)((f.n_part + f.run - 1) / f.run);
+        f.folded = f.room;
+        hipLaunchKernelGGL(norm_fold_kernel, dim3(f.folds + tensors), dim3(kFinishBlock), 0, s, f);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        f.part = f.folded;
+        f.n_part = f.folds;
+        tensors = 0;
     }
-    hipLaunchKernelGGL(norm_finish_kernel, dim3(grid), dim3(kFinishBlock), 0, s, f);
+    hipLaunchKernelGGL(norm_finish_kernel, dim3(1 + tensors), dim3(kFinishBlock), 0, s, f);
     return hipGetLastError();
 }
 
@@ -1115,18 +1174,7 @@ hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hi
         if (e != hipSuccess)
             return e;
     }
-    if (f.n_part > kFoldFrom) {
-        const int64_t run = (f.n_part + kFoldRuns - 1) / kFoldRuns;
-        double *out = a.part + f.n_part;
-        const int64_t runs = (f.n_part + run - 1) / run;
-        hipLaunchKernelGGL(norm_fold_kernel, dim3((unsigned)runs), dim3(kFinishBlock), 0, s, f.part,
-                           f.n_part, run, out);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess)
-            return e;
-        f.part = out;
-        f.n_part = runs;
-    }
+    f.room = a.part + f.n_part;
     return finish(f, s);
 }
 
@@ -1138,11 +1186,13 @@ int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t *passes)
     return all ? (all + *passes - 1) / *passes : 0;
 }
 
+int64_t norm_pieces_workspace(int64_t n_pieces) { return 8 * (n_pieces + fold_room(n_pieces)); }
+
 int64_t reduce_norm_workspace(int64_t n, zero_dtype gdt)
 {
     int64_t passes;
     const int64_t waves = reduce_norm_waves(n, gdt, &passes);
-    return 8 * (waves + (waves > kFoldFrom ? kFoldRuns : 0));
+    return 8 * (waves + fold_room(waves));
 }
 
 hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s)
@@ -1155,7 +1205,10 @@ hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s)
 {
     f.part = a.part;
     f.n_part = a.n_pieces;
+    f.room = a.part + a.n_pieces;
     f.pieces = a.pieces;
+    f.pieces_sq = a.part;
+    f.n_pieces = a.n_pieces;
     if (a.n_pieces > 0) {
         hipLaunchKernelGGL(norm_pieces_kernel, dim3(block_grid(a.n_pieces, kNormBlock)), dim3(kNormBlock), 0, s, a);
         const hipError_t e = hipGetLastError();

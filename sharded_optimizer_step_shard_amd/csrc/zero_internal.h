@@ -75,15 +75,21 @@ struct ReduceNormArgs {
 };
 
 // What becomes of n_part partial sums: the total, the coefficient, and, with
-// pieces given, each tensor's sum.
+// tensor_sq given, the sums of the tensors' pieces.  The launch sets the rest:
+// room for folded sums, and the folding.
 struct FinishArgs {
     const double *part;
     int64_t n_part;
     double *sq;
     ClipArgs clip;
     const zero_piece *pieces;
+    const double *pieces_sq;
+    int64_t n_pieces;
     double *tensor_sq;
     int64_t n_tensors;
+    double *room, *folded;
+    int64_t run;
+    unsigned folds;
 };
 
 struct PiecesArgs {
@@ -141,6 +147,7 @@ hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hi
 // of workspace that it uses.
 int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t *passes);
 int64_t reduce_norm_workspace(int64_t n, zero_dtype gdt);
+int64_t norm_pieces_workspace(int64_t n_pieces);
 hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s);
 hipError_t launch_norm_pieces(const PiecesArgs &a, FinishArgs f, hipStream_t s);
 hipError_t launch_scale_pieces(const PiecesArgs &a, hipStream_t s);

@@ -35,8 +35,8 @@ BAD_SPECS = [dict(max_norm=-1.0), dict(max_norm=NAN), dict(eps=-1e-9), dict(eps=
 
 def test_workspace_sizes():
     assert zs.zero_norm_workspace() >= 8 * zs.ZERO_NORM_PARTIALS
-    for n in (1, 24, zs.ZERO_NORM_PARTIALS + 1):
-        assert zs.zero_norm_workspace(n) == 8 * n
+    for n in (1, 24, 16384, 16385, zs.ZERO_NORM_PARTIALS + 1):
+        assert zs.zero_norm_workspace(n) == 8 * (n + (256 if n > 16384 else 0))
     for bad in (-1, 1 << 31):
         with pytest.raises(zs.ZeroShardError):
             zs.zero_norm_workspace(bad)

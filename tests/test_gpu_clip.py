@@ -676,3 +676,28 @@ def test_many_clipped_steps_in_a_row(zs, layout):
         s.step([dev(g)], torch.tensor([0.0, coef], dtype=torch.float64, device="cuda"), t=t)
         st, prm = oracle_step(layout, (g.astype(np.float64) * coef).astype(np.float32), st, prm, t)
         s.check(st, prm, f"step {t}")
+
+
+@pytest.mark.parametrize("kinds", ["bf16", "mixed"])
+def test_tensors_of_few_and_of_many_pieces(zs, kinds):
+    """Each way of adding a tensor's pieces (by a lane, a wave, a workgroup), at
+    its borders, in tables that are folded first and tables that are not."""
+    counts = [1, 4, 8, 9, 64, 65, 1, 1023, 1, 1024, 1025, 2, 0, 3000, 7, 1]
+    rng = np.random.default_rng(16)
+    for more in ([], [16400, 1, 7]):
+        c = counts + more
+        numels = [64 * k for k in c]
+        names = [("bf16", "fp16", "fp32")[i % 3] if kinds == "mixed" else kinds for i in range(len(c))]
+        flat = {k: torch.from_numpy(rng.standard_normal(sum(numels)).astype(np.float32)).to(DT[k]).cuda() for k in set(names)}
+        at, ts = 0, []
+        for n, k in zip(numels, names):
+            ts.append(flat[k][at:at + n])
+            at += n
+        table = zs.zero_build_pieces(ts, max_piece=64)
+        assert len(table) == sum(max(k, 1) for k in c)
+        sq, tsq = f64(), f64(len(ts))
+        zs.zero_norm_pieces(zs.pieces_to_device(table), len(table), sq, workspace(zs, len(table)), tensor_sq=tsq)
+        each = [math.fsum((t64(t) ** 2).tolist()) for t in ts]
+        near(sq.item(), math.fsum(each), "all")
+        for i, e in enumerate(each):
+            near(tsq[i].item(), e, f"tensor {i} of {c[i]} pieces")
