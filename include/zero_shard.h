@@ -196,9 +196,12 @@ enum {
 #define ZERO_SMALL_LAUNCH_CHUNKS 2048
 #define ZERO_SMALL_LAUNCH_CHUNKS_12B 16384
 /* Chunk length for the clipped steps on a reduced fp32 gradient (n_ranks = 1,
- * ZERO_FP32), and piece length for the calls over many tensors. */
+ * ZERO_FP32; 842M elements, fp32 master, m, v: 4.03 ms against 4.34 with 2048),
+ * and piece length for the calls over many tensors (2^29 bf16 elements summed
+ * in 149 us against 175 with 8192; scaling takes half a piece at a time). */
 #define ZERO_DEFAULT_MAX_CHUNK_REDUCED 1024
 #define ZERO_DEFAULT_MAX_PIECE 16384
+#define ZERO_MAX_PIECES (1 << 28)   /* largest table of pieces */
 /* Partial sums zero_reduce_norm_shard leaves in its workspace, at most: one a
  * wave, and a wave of its fastest shape takes 512 elements of bf16 or 256 of
  * fp32, so that shards up to 2^30 (2^29) elements run in that shape. */
@@ -535,7 +538,7 @@ int zero_gather_write(const float *master, int64_t shard_len, const zero_chunk *
  * run at the same time (other streams, graphs replayed side by side) need a
  * workspace each.
  */
-int64_t zero_norm_workspace(int64_t n_pieces);   /* -1 for n_pieces outside [0, INT32_MAX] */
+int64_t zero_norm_workspace(int64_t n_pieces);   /* -1 for n_pieces outside [0, ZERO_MAX_PIECES] */
 
 /*
  * zero_reduce_shard with the sum of squares in the same pass:
@@ -632,12 +635,12 @@ int zero_shard_step_kahan_scheduled_clipped(const void *const *partials, int n_r
  * both NULL for in place (zero_norm_pieces writes neither way).
  * Tensors are cut every max_piece elements (a positive multiple of 64, at most
  * 2^24), the first piece shorter so that the others start 16-byte aligned in
- * dst; an empty tensor has one piece of length 0.  A contiguous run of the table that ends where a
- * tensor ends may be passed alone.
+ * dst; an empty tensor has one piece of length 0.  A contiguous run of the
+ * table may be passed alone; a tensor's sum then needs all of its pieces in it.
  * out, cap, n_out: as zero_build_chunks.
  * Errors: INVALID (a NULL array, n_tensors < 0, a negative count or a total
  * above ZERO_MAX_LEN, a NULL address of a non-empty tensor, one of dst and
- * dst_dt NULL, a bad max_piece), MISALIGNED (an address its element size does
+ * dst_dt NULL, a bad max_piece, more than ZERO_MAX_PIECES pieces), MISALIGNED (an address its element size does
  * not divide), UNSUPPORTED (a type), ALIAS (a tensor's place overlaps another's
  * place or any tensor, unless it is exactly its own tensor in its own type),
  * CAPACITY.
@@ -656,7 +659,7 @@ int zero_build_pieces(const void *const *src, const int *src_dt, void *const *ds
  * [0, 2^24] or an unknown type count as empty; the addresses in the table
  * are otherwise trusted.
  * Errors: INVALID (NULL sq or workspace, a NULL table of n_pieces > 0, n_pieces
- * or n_tensors outside [0, INT32_MAX], a bad spec), CAPACITY (workspace),
+ * outside [0, ZERO_MAX_PIECES], n_tensors outside [0, INT32_MAX], a bad spec), CAPACITY (workspace),
  * MISALIGNED, ALIAS (outputs, workspace and table overlap), NOT_DEVICE, HIP.
  */
 int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, double *tensor_sq,
@@ -669,7 +672,7 @@ int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, d
  * With a NaN coef nothing is written; with coef = 1 pieces in place are not
  * touched (they are what they would be).
  * Errors: INVALID (NULL clip, a NULL table of n_pieces > 0, n_pieces outside
- * [0, INT32_MAX]), MISALIGNED, NOT_DEVICE, HIP.
+ * [0, ZERO_MAX_PIECES]), MISALIGNED, NOT_DEVICE, HIP.
  */
 int zero_scale_pieces(const zero_piece *d_pieces, int64_t n_pieces, const double *clip,
                       hipStream_t stream);

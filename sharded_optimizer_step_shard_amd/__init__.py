@@ -37,6 +37,7 @@ ZERO_SMALL_LAUNCH_CHUNKS_12B = 16384   # 12-byte step
 ZERO_DEFAULT_MAX_CHUNK_REDUCED = 1024  # clipped steps on a reduced fp32 gradient
 ZERO_DEFAULT_MAX_PIECE = 16384         # calls over many tensors
 ZERO_NORM_PARTIALS = 1 << 21
+ZERO_MAX_PIECES = 1 << 28
 ZERO_PROBE_SUM_MAX = 16
 
 # Mirrors `zero_chunk` (32 bytes).
@@ -186,6 +187,18 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream
 
 
+def _stream_here(stream, x) -> Optional[int]:
+    """_stream, for a call on tensor x: without a stream the call would go to
+    the current device's, which has to be x's."""
+    if stream is None and not isinstance(x, (int, np.integer, tuple)) and x is not None:
+        import torch
+        if x.get_device() != torch.cuda.current_device():
+            raise ValueError(f"tensors on device {x.get_device()} while device "
+                             f"{torch.cuda.current_device()} is current: pass a stream of theirs, "
+                             "or make their device current")
+    return _stream(stream)
+
+
 def _gdt_of(partials) -> int:
     p0 = partials[0]
     if isinstance(p0, (int, np.integer)):
@@ -297,12 +310,13 @@ def zero_reduce_norm_shard(partials: Sequence[Ptr], n: int, sq: Ptr, workspace,
     ws, ws_bytes = _byte_range(workspace)
     _check(_lib.zero_reduce_norm_shard(_partial_array(partials), len(partials), gdt,
                                        ctypes.byref(rs), n, _addr(grad_out), _addr(sq), _spec(spec),
-                                       ws, ws_bytes, _stream(stream)), "zero_reduce_norm_shard")
+                                       ws, ws_bytes, _stream_here(stream, workspace)),
+           "zero_reduce_norm_shard")
 
 
 def zero_clip_coef(sq: Ptr, n_sq: int, spec: ClipSpec, stream=None) -> None:
     """Norm and coefficient of n_sq sums of squares, into the spec's out."""
-    _check(_lib.zero_clip_coef(_addr(sq), n_sq, _spec(spec), _stream(stream)), "zero_clip_coef")
+    _check(_lib.zero_clip_coef(_addr(sq), n_sq, _spec(spec), _stream_here(stream, sq)), "zero_clip_coef")
 
 
 def _dense_addr(t) -> int:
@@ -368,13 +382,13 @@ def zero_norm_pieces(d_pieces: Ptr, n_pieces: int, sq: Ptr, workspace, tensor_sq
     ws, ws_bytes = _byte_range(workspace)
     _check(_lib.zero_norm_pieces(_addr(d_pieces), n_pieces, _addr(sq), _addr(tensor_sq),
                                  0 if tensor_sq is None else tensor_sq.numel(), _spec(spec), ws,
-                                 ws_bytes, _stream(stream)), "zero_norm_pieces")
+                                 ws_bytes, _stream_here(stream, workspace)), "zero_norm_pieces")
 
 
 def zero_scale_pieces(d_pieces: Ptr, n_pieces: int, clip: Ptr, stream=None) -> None:
     """Every piece times clip[1], into its place."""
-    _check(_lib.zero_scale_pieces(_addr(d_pieces), n_pieces, _addr(clip), _stream(stream)),
-           "zero_scale_pieces")
+    _check(_lib.zero_scale_pieces(_addr(d_pieces), n_pieces, _addr(clip),
+                                  _stream_here(stream, clip)), "zero_scale_pieces")
 
 
 def _step_clipped(name: str, partials, state, shard_len: int, d_chunks: Ptr, n_chunks: int, consts,
@@ -382,7 +396,7 @@ def _step_clipped(name: str, partials, state, shard_len: int, d_chunks: Ptr, n_c
     gdt = _gdt_of(partials) if gdt is None else gdt
     _check(getattr(_lib, name)(_partial_array(partials), len(partials), gdt, *map(_addr, state),
                                shard_len, _addr(d_chunks), n_chunks, *consts, _addr(clip),
-                               _stream(stream)), name)
+                               _stream_here(stream, clip)), name)
 
 
 def zero_shard_step_clipped(partials: Sequence[Ptr], master: Ptr, m: Ptr, v: Ptr, shard_len: int,

@@ -674,7 +674,7 @@ int zero_shard_step_kahan_scheduled_clipped(const void *const *partials, int n_r
 
 int64_t zero_norm_workspace(int64_t n_pieces)
 {
-    if (n_pieces < 0 || n_pieces > INT32_MAX)
+    if (n_pieces < 0 || n_pieces > ZERO_MAX_PIECES)
         return -1;
     return n_pieces ? norm_pieces_workspace(n_pieces) : reduce_norm_workspace(ZERO_MAX_LEN, ZERO_FP32);
 }
@@ -749,7 +749,7 @@ int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, d
                      int64_t n_tensors, const zero_clip_spec *spec, void *workspace,
                      int64_t workspace_bytes, hipStream_t stream)
 {
-    if (n_pieces < 0 || n_pieces > INT32_MAX || (n_pieces > 0 && !d_pieces) || n_tensors < 0 ||
+    if (n_pieces < 0 || n_pieces > ZERO_MAX_PIECES || (n_pieces > 0 && !d_pieces) || n_tensors < 0 ||
         n_tensors > INT32_MAX || !sq || !workspace || workspace_bytes < 0 ||
         (spec && !valid_clip_spec(spec)))
         return ZERO_ERR_INVALID;
@@ -784,7 +784,7 @@ int zero_norm_pieces(const zero_piece *d_pieces, int64_t n_pieces, double *sq, d
 int zero_scale_pieces(const zero_piece *d_pieces, int64_t n_pieces, const double *clip,
                       hipStream_t stream)
 {
-    if (n_pieces < 0 || n_pieces > INT32_MAX || (n_pieces > 0 && !d_pieces) || !clip)
+    if (n_pieces < 0 || n_pieces > ZERO_MAX_PIECES || (n_pieces > 0 && !d_pieces) || !clip)
         return ZERO_ERR_INVALID;
     if (!aligned16(d_pieces) || !aligned16(clip))
         return ZERO_ERR_MISALIGNED;

@@ -19,6 +19,15 @@ int64_t dtype_bytes(int dt)
     return dt == ZERO_BF16 || dt == ZERO_FP16 ? 2 : (dt == ZERO_FP32 ? 4 : 0);
 }
 
+// Elements by which an address is past a 16-byte boundary.
+int64_t past_boundary(const void *p, int64_t bytes) { return (int64_t)((uintptr_t)p & 15u) / bytes; }
+
+// Pieces of a tensor of n elements whose first is shorter by `past`.
+int64_t pieces_of(int64_t n, int64_t past, int64_t max_piece)
+{
+    return n == 0 ? 1 : (n + past + max_piece - 1) / max_piece;
+}
+
 // Does any of `ranges` (sorted by start, disjoint) meet r?
 bool meets(const std::vector<Range> &ranges, const Range &r)
 {
@@ -89,6 +98,15 @@ int zero_build_pieces(const void *const *src, const int *src_dt, void *const *ds
     for (int t = 0; t < n_tensors; ++t)
         if (!dtype_bytes(src_dt[t]) || (dst && !dtype_bytes(dst_dt[t])))
             return ZERO_ERR_UNSUPPORTED;
+    // pieces in all, before the table itself: a tensor's first piece is shorter
+    // by the elements its place is past a 16-byte boundary
+    int64_t pieces_all = 0;
+    for (int t = 0; t < n_tensors; ++t) {
+        const int64_t db = dtype_bytes(dst ? dst_dt[t] : src_dt[t]);
+        pieces_all += pieces_of(numels[t], past_boundary(dst ? dst[t] : src[t], db), max_piece);
+    }
+    if (pieces_all > ZERO_MAX_PIECES)
+        return ZERO_ERR_INVALID;
     try {
         const int rc = check_places(src, src_dt, dst, dst_dt, numels, n_tensors);
         if (rc)
@@ -102,10 +120,8 @@ int zero_build_pieces(const void *const *src, const int *src_dt, void *const *ds
         const int ddt = dst ? dst_dt[t] : src_dt[t];
         const int64_t sb = dtype_bytes(src_dt[t]), db = dtype_bytes(ddt);
         char *d = (char *)(dst ? dst[t] : (void *)src[t]);
-        // elements by which dst is past a 16-byte boundary: the first piece is
-        // shorter by them, so that every other piece starts on one
-        const int64_t past = (int64_t)((uintptr_t)d & 15u) / db;
-        const int64_t pieces = numels[t] == 0 ? 1 : (numels[t] + past + max_piece - 1) / max_piece;
+        const int64_t past = past_boundary(d, db);
+        const int64_t pieces = pieces_of(numels[t], past, max_piece);
         int64_t at = 0;
         for (int64_t p = 0; p < pieces; ++p, ++count) {
             int64_t end = (p + 1) * max_piece - past;
@@ -117,7 +133,7 @@ int zero_build_pieces(const void *const *src, const int *src_dt, void *const *ds
                 c.dst = d + at * db;
                 c.len = (int32_t)(end - at);
                 c.tensor_id = t;
-                c.tensor_pieces = p == 0 ? (int32_t)(pieces < INT32_MAX ? pieces : INT32_MAX) : 0;
+                c.tensor_pieces = p == 0 ? (int32_t)pieces : 0;
                 c.src_dt = (int16_t)src_dt[t];
                 c.dst_dt = (int16_t)ddt;
             }

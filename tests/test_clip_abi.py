@@ -6,12 +6,22 @@ import ctypes
 import numpy as np
 import pytest
 
-import sharded_optimizer_step_shard_amd as zs
-
 BASE = 0x7F0000000000
-INVALID, MISALIGNED, UNSUPPORTED = zs.ZERO_ERR_INVALID, zs.ZERO_ERR_MISALIGNED, zs.ZERO_ERR_UNSUPPORTED
-ALIAS, CAPACITY, NOT_DEVICE = zs.ZERO_ERR_ALIAS, zs.ZERO_ERR_CAPACITY, zs.ZERO_ERR_NOT_DEVICE
+INVALID, MISALIGNED, UNSUPPORTED, ALIAS, CAPACITY, NOT_DEVICE = 1, 2, 3, 4, 6, 7
+zs = None
 INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    """Loaded when a test runs, not while tests are collected: GPU tests in the
+    same process have to load torch's HIP runtime first."""
+    global zs
+    import sharded_optimizer_step_shard_amd as m
+    zs = m
+    assert (INVALID, MISALIGNED, UNSUPPORTED, ALIAS, CAPACITY, NOT_DEVICE) == (
+        m.ZERO_ERR_INVALID, m.ZERO_ERR_MISALIGNED, m.ZERO_ERR_UNSUPPORTED, m.ZERO_ERR_ALIAS, m.ZERO_ERR_CAPACITY,
+        m.ZERO_ERR_NOT_DEVICE)
 
 
 def at(k):
@@ -37,7 +47,7 @@ def test_workspace_sizes():
     assert zs.zero_norm_workspace() >= 8 * zs.ZERO_NORM_PARTIALS
     for n in (1, 24, 16384, 16385, zs.ZERO_NORM_PARTIALS + 1):
         assert zs.zero_norm_workspace(n) == 8 * (n + (256 if n > 16384 else 0))
-    for bad in (-1, 1 << 31):
+    for bad in (-1, zs.ZERO_MAX_PIECES + 1):
         with pytest.raises(zs.ZeroShardError):
             zs.zero_norm_workspace(bad)
 
@@ -145,7 +155,7 @@ def test_norm_pieces_refusals():
     def call(pieces=at(1), n=10, sq=at(2), tsq=at(3), n_tensors=5, sp=None, ws=at(4), ws_bytes=1 << 20):
         return zs.raw_call("zero_norm_pieces", pieces, n, sq, tsq, n_tensors, sp, ws, ws_bytes, None)
     assert call() == NOT_DEVICE and call(tsq=None, n_tensors=0) == NOT_DEVICE and call(sp=spec()) == NOT_DEVICE
-    for bad in (dict(pieces=None), dict(n=-1), dict(n=1 << 31), dict(sq=None), dict(ws=None),
+    for bad in (dict(pieces=None), dict(n=-1), dict(n=(1 << 28) + 1), dict(sq=None), dict(ws=None),
                 dict(n_tensors=-1), dict(n_tensors=1 << 31), dict(ws_bytes=-8)):
         assert call(**bad) == INVALID, bad
     for bad in BAD_SPECS:
@@ -162,7 +172,7 @@ def test_norm_pieces_refusals():
 def test_scale_pieces_refusals():
     call = lambda p=at(1), n=10, c=at(2): zs.raw_call("zero_scale_pieces", p, n, c, None)
     assert call() == NOT_DEVICE
-    assert call(p=None) == INVALID and call(n=-1) == INVALID and call(n=1 << 31) == INVALID and call(c=None) == INVALID
+    assert call(p=None) == INVALID and call(n=-1) == INVALID and call(n=(1 << 28) + 1) == INVALID and call(c=None) == INVALID
     assert call(p=at(1) + 8) == MISALIGNED and call(c=at(2) + 8) == MISALIGNED
     assert call(p=None, n=0) == zs.ZERO_OK
 
@@ -191,7 +201,8 @@ def test_build_pieces_refusals():
                 dict(src=[a], sdt=[0], numels=[4], dst=[None], ddt=[0]),
                 dict(src=[a, b], sdt=[0, 0], numels=[1 << 48, 1]),
                 dict(src=[a], sdt=[0], numels=[4], max_piece=0), dict(src=[a], sdt=[0], numels=[4], max_piece=100),
-                dict(src=[a], sdt=[0], numels=[4], max_piece=(1 << 24) + 64)):
+                dict(src=[a], sdt=[0], numels=[4], max_piece=(1 << 24) + 64),
+                dict(src=[a], sdt=[0], numels=[64 * (1 << 28) + 1], max_piece=64)):
         assert build(**bad)[0] == INVALID, bad
     assert build([a + 1], [0], [4])[0] == MISALIGNED and build([a + 2], [1], [4])[0] == MISALIGNED
     assert build([a], [0], [4], [b + 2], [1])[0] == MISALIGNED
@@ -272,3 +283,27 @@ def test_scheduled_and_plain_clipped_steps_are_declared_together():
     for name in STEPS:
         for f in (name + "_clipped", name + "_scheduled_clipped"):
             assert hasattr(zs, f) and hasattr(zs.lib(), f)
+
+
+def test_tensors_on_a_device_that_is_not_current_are_refused(monkeypatch):
+    torch = pytest.importorskip("torch")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    class On1:
+        is_cuda = True
+        def is_contiguous(self): return True
+        def data_ptr(self): return at(1)
+        def get_device(self): return 1
+        def numel(self): return 4
+        def element_size(self): return 8
+
+    t = On1()
+    sp = zs.ClipSpec(1.0, 1e-6, 1.0, at(90))
+    for call in (lambda **k: zs.zero_clip_coef(t, 4, sp, **k), lambda **k: zs.zero_scale_pieces(at(2), 1, t, **k),
+                 lambda **k: zs.zero_norm_pieces(at(2), 1, at(3), t, **k),
+                 lambda **k: zs.zero_reduce_norm_shard([at(4)], 1, at(3), t, gdt=0, **k),
+                 lambda **k: zs.zero_shard_step_clipped([at(4)], at(5), at(6), at(7), 8, at(8), 1, zs.hparams(1), t, gdt=0, **k)):
+        with pytest.raises(ValueError, match="device 1 while device 0"):
+            call()
+        with pytest.raises(zs.ZeroShardError):       # a stream of its own is taken; the fake addresses are not
+            call(stream=0x1000)
