@@ -527,8 +527,8 @@ int zero_gather_write(const float *master, int64_t shard_len, const zero_chunk *
  * Slides 19-20).
  *
  * Sums of squares are formed in double from exact squares (an fp32 value
- * squared is exact in double) in an order fixed by the element count or the
- * table, so the same call gives the same bits every time.
+ * squared is exact in double) in an order that follows from the arguments
+ * alone, so the same call gives the same bits every time.
  *
  * Workspace: device memory, 16-byte aligned: zero_norm_workspace(n_pieces)
  * bytes for zero_norm_pieces; zero_norm_workspace(0), 16 MiB and a little, is

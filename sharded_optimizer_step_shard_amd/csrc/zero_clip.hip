@@ -1166,7 +1166,14 @@ hipError_t step_clip_layout(const StepArgs &a, zero_dtype gdt, hipStream_t s)
 hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hipStream_t s)
 {
     f.part = a.part;
-    f.n_part = reduce_norm_waves(a.n, gdt, &a.passes);
+    // With nothing to store, and so nothing that the next pass's loads wait for, a
+    // wave takes about 8 loads, two passes at least (132M elements, one pass
+    // against this: one bf16 partial 87 / 60 us, two 108 / 83, four 172 / 155,
+    // eight 338 / 305).
+    int64_t least = 1;
+    if (!a.out && a.red.n_ranks <= 16)
+        least = a.red.n_ranks < 4 ? 8 / a.red.n_ranks : 2;
+    f.n_part = reduce_norm_waves(a.n, gdt, least, &a.passes);
     if (f.n_part > 0) {
         const dim3 grid((unsigned)f.n_part);
         const hipError_t e = gdt == ZERO_BF16 ? reduce_norm_dispatch<ZERO_BF16>(a, grid, s)
@@ -1178,11 +1185,18 @@ hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hi
     return finish(f, s);
 }
 
-int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t *passes)
+// Eight waves on each of 1024 SIMDs.
+constexpr int64_t kFewWaves = 8192;
+
+int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t least, int64_t *passes)
 {
     const int64_t pass = kStepLanes * (gdt == ZERO_BF16 ? Grad<ZERO_BF16>::VEC : Grad<ZERO_FP32>::VEC);
     const int64_t all = (n + pass - 1) / pass;
     *passes = (all + ZERO_NORM_PARTIALS - 1) / ZERO_NORM_PARTIALS;
+    if (least > all / kFewWaves)   // but no fewer waves than fill the GPU
+        least = all / kFewWaves;
+    if (*passes < least)
+        *passes = least;
     return all ? (all + *passes - 1) / *passes : 0;
 }
 
@@ -1191,7 +1205,7 @@ int64_t norm_pieces_workspace(int64_t n_pieces) { return 8 * (n_pieces + fold_ro
 int64_t reduce_norm_workspace(int64_t n, zero_dtype gdt)
 {
     int64_t passes;
-    const int64_t waves = reduce_norm_waves(n, gdt, &passes);
+    const int64_t waves = reduce_norm_waves(n, gdt, 1, &passes);
     return 8 * (waves + fold_room(waves));
 }
 

@@ -143,9 +143,9 @@ hipError_t launch_adamw(const AdamArgs &a, hipStream_t s);
 hipError_t launch_gather(const GatherArgs &a, hipStream_t s);
 hipError_t launch_step_clipped(const StepArgs &a, zero_dtype gdt, StateLayout layout, hipStream_t s);
 hipError_t launch_reduce_norm(ReduceNormArgs a, zero_dtype gdt, FinishArgs f, hipStream_t s);
-// Waves of that launch over n elements, each of *passes passes, and the bytes
-// of workspace that it uses.
-int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t *passes);
+// Waves of that launch over n elements, each of *passes >= least passes, and
+// the bytes of workspace that is enough for any `least`.
+int64_t reduce_norm_waves(int64_t n, zero_dtype gdt, int64_t least, int64_t *passes);
 int64_t reduce_norm_workspace(int64_t n, zero_dtype gdt);
 int64_t norm_pieces_workspace(int64_t n_pieces);
 hipError_t launch_clip_coef(const double *sq, int64_t n, const ClipArgs &c, hipStream_t s);

@@ -701,3 +701,16 @@ def test_tensors_of_few_and_of_many_pieces(zs, kinds):
         near(sq.item(), math.fsum(each), "all")
         for i, e in enumerate(each):
             near(tsq[i].item(), e, f"tensor {i} of {c[i]} pieces")
+
+
+@pytest.mark.parametrize("ranks", [1, 2, 3, 8, 16, 20])
+def test_the_norm_alone_in_several_passes(zs, ranks):
+    """Without a gradient to store a wave takes more passes; around where it
+    starts to, and with a short last pass."""
+    for n in (512 * 8192 - 5, 512 * 8192 * 2 + 3, 512 * 8192 * 9 // 2 + 513):
+        gen = torch.Generator("cuda").manual_seed(n)
+        p = [torch.empty(n, dtype=torch.bfloat16, device="cuda").normal_(0, 1e-3, generator=gen) for _ in range(ranks)]
+        sq, g = f64(), torch.empty(n, device="cuda")
+        zs.zero_reduce_shard(p, n, g)
+        zs.zero_reduce_norm_shard(p, n, sq, workspace(zs))
+        near(sq.item(), math.fsum(np.square(g.double().cpu().numpy())), f"{ranks} ranks, {n}")
