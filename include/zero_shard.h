@@ -520,8 +520,10 @@ int zero_gather_write(const float *master, int64_t shard_len, const zero_chunk *
  *   zero_clip_coef           norm and coefficient, on the device
  *   zero_shard_step_clipped  from g: partials = {g}, n_ranks = 1, ZERO_FP32
  *
- * with no value read back by the host.  The gradients are averaged over the
- * ranks before they are clipped, since the full-batch gradient is their mean
+ * with no value read back by the host.  (A two-level order or an accumulator
+ * goes into the reduce; gradient buckets cannot be stepped before the last of
+ * them is known, so neither needs a clipped step of its own.)  The gradients
+ * are averaged over the ranks before they are clipped, since the full-batch gradient is their mean
  * ("并行策略总览：六个维度各切什么、怎么通信", data-parallel section), and each rank
  * clips the segment it owns ("CS336 2026 Lecture 8: Parallelism Basics",
  * Slides 19-20).

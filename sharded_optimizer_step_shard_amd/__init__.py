@@ -279,11 +279,28 @@ def _partial_array(partials):
     return (ctypes.c_void_p * max(len(addrs), 1))(*addrs)
 
 
+def _floats(x: Ptr, size: int, n: int, what: str) -> Optional[int]:
+    """_addr of an array of n floating values of `size` bytes; of a tensor, type
+    and length are checked (a call would write past the end of a short one)."""
+    if x is not None and not isinstance(x, (int, np.integer)):
+        dt = x.dtype
+        if dt.itemsize != size or not dt.is_floating_point or x.numel() < n:
+            raise ValueError(f"{what} must hold {n} values of float{8 * size}, not {x.numel()} of {dt}")
+    return _addr(x)
+
+
+def _table(d_pieces: Ptr, n_pieces: int) -> Optional[int]:
+    if d_pieces is not None and not isinstance(d_pieces, (int, np.integer)):
+        if d_pieces.numel() * d_pieces.element_size() < n_pieces * PIECE_DTYPE.itemsize:
+            raise ValueError(f"the table holds fewer than {n_pieces} pieces")
+    return _addr(d_pieces)
+
+
 def clip_spec(out: Ptr, max_norm: float, eps: float = 1e-6, inv_scale: float = 1.0) -> ClipSpec:
     """What the clipping coefficient is formed with; `out` (two doubles on the
     device) receives the norm and the coefficient.  The caller keeps `out`
     alive while calls use the spec, as with every array."""
-    return ClipSpec(max_norm, eps, inv_scale, _addr(out))
+    return ClipSpec(max_norm, eps, inv_scale, _floats(out, 8, 2, "out"))
 
 
 def zero_norm_workspace(n_pieces: int = 0) -> int:
@@ -306,17 +323,18 @@ def zero_reduce_norm_shard(partials: Sequence[Ptr], n: int, sq: Ptr, workspace,
     """Reduced gradient (to grad_out, unless None) and its sum of squares in
     one pass; workspace: a tensor or an (address, bytes) pair."""
     gdt = _gdt_of(partials) if gdt is None else gdt
-    rs = ReduceSpec(group, micro_batches, _addr(acc))
+    rs = ReduceSpec(group, micro_batches, _floats(acc, 4, n, "acc"))
     ws, ws_bytes = _byte_range(workspace)
     _check(_lib.zero_reduce_norm_shard(_partial_array(partials), len(partials), gdt,
-                                       ctypes.byref(rs), n, _addr(grad_out), _addr(sq), _spec(spec),
-                                       ws, ws_bytes, _stream_here(stream, workspace)),
+                                       ctypes.byref(rs), n, _floats(grad_out, 4, n, "grad_out"),
+                                       _floats(sq, 8, 1, "sq"), _spec(spec), ws, ws_bytes, _stream_here(stream, workspace)),
            "zero_reduce_norm_shard")
 
 
 def zero_clip_coef(sq: Ptr, n_sq: int, spec: ClipSpec, stream=None) -> None:
     """Norm and coefficient of n_sq sums of squares, into the spec's out."""
-    _check(_lib.zero_clip_coef(_addr(sq), n_sq, _spec(spec), _stream_here(stream, sq)), "zero_clip_coef")
+    _check(_lib.zero_clip_coef(_floats(sq, 8, n_sq, "sq"), n_sq, _spec(spec),
+                               _stream_here(stream, sq)), "zero_clip_coef")
 
 
 def _dense_addr(t) -> int:
@@ -380,14 +398,16 @@ def zero_norm_pieces(d_pieces: Ptr, n_pieces: int, sq: Ptr, workspace, tensor_sq
     """Sum of squares of many tensors into sq, each tensor's into tensor_sq
     (a float64 tensor, one element a tensor), and the coefficient if spec."""
     ws, ws_bytes = _byte_range(workspace)
-    _check(_lib.zero_norm_pieces(_addr(d_pieces), n_pieces, _addr(sq), _addr(tensor_sq),
+    _check(_lib.zero_norm_pieces(_table(d_pieces, n_pieces), n_pieces, _floats(sq, 8, 1, "sq"),
+                                 _floats(tensor_sq, 8, 0, "tensor_sq"),
                                  0 if tensor_sq is None else tensor_sq.numel(), _spec(spec), ws,
                                  ws_bytes, _stream_here(stream, workspace)), "zero_norm_pieces")
 
 
 def zero_scale_pieces(d_pieces: Ptr, n_pieces: int, clip: Ptr, stream=None) -> None:
     """Every piece times clip[1], into its place."""
-    _check(_lib.zero_scale_pieces(_addr(d_pieces), n_pieces, _addr(clip),
+    _check(_lib.zero_scale_pieces(_table(d_pieces, n_pieces), n_pieces,
+                                  _floats(clip, 8, 2, "clip"),
                                   _stream_here(stream, clip)), "zero_scale_pieces")
 
 
@@ -395,8 +415,8 @@ def _step_clipped(name: str, partials, state, shard_len: int, d_chunks: Ptr, n_c
                   clip: Ptr, gdt: Optional[int], stream) -> None:
     gdt = _gdt_of(partials) if gdt is None else gdt
     _check(getattr(_lib, name)(_partial_array(partials), len(partials), gdt, *map(_addr, state),
-                               shard_len, _addr(d_chunks), n_chunks, *consts, _addr(clip),
-                               _stream_here(stream, clip)), name)
+                               shard_len, _addr(d_chunks), n_chunks, *consts,
+                               _floats(clip, 8, 2, "clip"), _stream_here(stream, clip)), name)
 
 
 def zero_shard_step_clipped(partials: Sequence[Ptr], master: Ptr, m: Ptr, v: Ptr, shard_len: int,

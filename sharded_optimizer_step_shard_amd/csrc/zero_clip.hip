@@ -8,9 +8,11 @@
 // the sums are kept in double: they can neither overflow nor lose small terms
 // before some 2^29 equal ones, and the double pipe has room beside the stream.
 //
-// Sums without atomics: each workgroup (one wave) leaves one double, and one
-// workgroup of a second launch adds those in a fixed order.  The order depends
-// on the element count or the table alone, so results repeat bit for bit.
+// Sums without atomics: each workgroup leaves one double, and one workgroup of a
+// later launch adds those in a fixed order that follows from the call's
+// arguments, so results repeat bit for bit.  Nothing is kept between calls, so
+// the workspace needs no clearing; a counter in it would save the small calls
+// their second launch (2 us) and give a wrong norm to who forgets to clear it.
 
 #include "zero_device.h"
 
@@ -386,7 +388,6 @@ __device__ __forceinline__ u32x2 ld_any2(const void *p)
 
 __device__ __forceinline__ void st_any(void *p, u32x4 x) { __builtin_nontemporal_store(x, (u32x4_any *)p); }
 __device__ __forceinline__ void st_any(void *p, u32x2 x) { __builtin_nontemporal_store(x, (u32x2_any *)p); }
-
 
 __device__ __forceinline__ double half_to_double(uint32_t h)
 {

@@ -290,12 +290,22 @@ def test_tensors_on_a_device_that_is_not_current_are_refused(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
 
     class On1:
-        is_cuda = True
-        def is_contiguous(self): return True
-        def data_ptr(self): return at(1)
-        def get_device(self): return 1
-        def numel(self): return 4
-        def element_size(self): return 8
+        is_cuda, dtype = True, torch.float64
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return at(1)
+
+        def get_device(self):
+            return 1
+
+        def numel(self):
+            return 4
+
+        def element_size(self):
+            return 8
 
     t = On1()
     sp = zs.ClipSpec(1.0, 1e-6, 1.0, at(90))
@@ -307,3 +317,41 @@ def test_tensors_on_a_device_that_is_not_current_are_refused(monkeypatch):
             call()
         with pytest.raises(zs.ZeroShardError):       # a stream of its own is taken; the fake addresses are not
             call(stream=0x1000)
+
+
+def test_the_binding_refuses_arrays_of_another_type_or_size():
+    torch = pytest.importorskip("torch")
+
+    class Fake:
+        is_cuda = True
+
+        def __init__(self, dtype, n):
+            self.dtype, self.n = dtype, n
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return at(1)
+
+        def numel(self):
+            return self.n
+
+        def element_size(self):
+            return self.dtype.itemsize
+
+    f64, f32 = (lambda n: Fake(torch.float64, n)), (lambda n: Fake(torch.float32, n))
+    sp, ws = zs.ClipSpec(1.0, 1e-6, 1.0, at(90)), (at(3), 1 << 20)
+    reduce = lambda **k: zs.zero_reduce_norm_shard([at(4)], 10, k.pop("sq", at(2)), ws, gdt=0, stream=0, **k)
+    norm = lambda table=at(5), **k: zs.zero_norm_pieces(table, 3, k.pop("sq", at(2)), ws, stream=0, **k)
+    step = lambda clip: zs.zero_shard_step_kahan_clipped([at(4)], at(5), at(6), at(7), 8, at(8), 1, zs.hparams(1), clip, gdt=0, stream=0)
+    for bad in (lambda: zs.clip_spec(f32(2), 1.0), lambda: zs.clip_spec(f64(1), 1.0), lambda: reduce(sq=f32(1)), lambda: reduce(grad_out=f32(9)),
+                lambda: reduce(grad_out=f64(10)), lambda: reduce(acc=f32(9), micro_batches=2), lambda: zs.zero_clip_coef(f64(3), 4, sp, stream=0),
+                lambda: norm(sq=f32(4)), lambda: norm(tensor_sq=f32(4)), lambda: norm(table=Fake(torch.uint8, 95)),
+                lambda: zs.zero_scale_pieces(Fake(torch.uint8, 95), 3, at(2), stream=0), lambda: zs.zero_scale_pieces(at(5), 3, f64(1), stream=0),
+                lambda: step(f32(2)), lambda: step(f64(1))):
+        with pytest.raises(ValueError, match="must hold|fewer than"):
+            bad()
+    for good in (lambda: reduce(sq=f64(1)), lambda: norm(table=Fake(torch.uint8, 96)), lambda: norm(tensor_sq=f64(5)), lambda: step(f64(2))):
+        with pytest.raises(zs.ZeroShardError):       # the fake addresses
+            good()

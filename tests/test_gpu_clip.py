@@ -714,3 +714,44 @@ def test_the_norm_alone_in_several_passes(zs, ranks):
         zs.zero_reduce_shard(p, n, g)
         zs.zero_reduce_norm_shard(p, n, sq, workspace(zs))
         near(sq.item(), math.fsum(np.square(g.double().cpu().numpy())), f"{ranks} ranks, {n}")
+
+
+def test_a_table_longer_than_the_grid(zs):
+    """More pieces than workgroups are launched: each workgroup takes several.
+    Powers of two, so that every sum is exact."""
+    count = (1 << 22) + 1000
+    x = torch.full((64 * count,), 0.5, dtype=torch.bfloat16, device="cuda")
+    x[-1], x[0] = 4.0, 2.0
+    table = zs.zero_build_pieces([x[:64 * 1000], x[64 * 1000:]], max_piece=64)
+    assert len(table) == count
+    d, sq, tsq = zs.pieces_to_device(table), f64(), f64(2)
+    zs.zero_norm_pieces(d, count, sq, workspace(zs, count), tensor_sq=tsq)
+    assert tsq.tolist() == [(64000 - 1) * 0.25 + 4.0, (x.numel() - 64000 - 1) * 0.25 + 16.0] and sq.item() == tsq.sum().item()
+    zs.zero_scale_pieces(d, count, torch.tensor([0.0, 0.25], dtype=torch.float64, device="cuda"))
+    assert x[0] == 0.5 and x[-1] == 1.0 and (x[1:-1] == 0.125).all()
+
+
+def test_a_chunk_table_of_long_and_short_chunks(zs):
+    """Chunks that start and end off the group grid, in an order of their own,
+    with gaps between them that no chunk covers and that stay as they are."""
+    n = 20011
+    rng = np.random.default_rng(17)
+    cuts = np.sort(rng.choice(np.arange(1, n), 40, replace=False))
+    edges = [0, *cuts.tolist(), n]
+    spans = [(a, b) for k, (a, b) in enumerate(zip(edges[:-1], edges[1:])) if k % 5 != 3]
+    for layout in sorted(NAMES):
+        for gdt in ("fp32", "bf16"):
+            s = Shard(zs, layout, n, 5)
+            table = np.zeros(len(spans), dtype=zs.CHUNK_DTYPE)
+            for row, (a, b) in zip(table, [spans[i] for i in rng.permutation(len(spans))]):
+                row["shard_off"], row["len"], row["dst"] = a, b - a, s.slot.data_ptr() + 2 * (s.skew + a)
+            s.chunks, s.n_chunks = zs.chunks_to_device(table), len(table)
+            p = partials_of(rng, n, 1 if gdt == "fp32" else 4, gdt)
+            s.step([dev(x) for x in p], torch.tensor([0.0, 0.6], dtype=torch.float64, device="cuda"), gdt=0 if gdt == "bf16" else 1)
+            gc = (oracle.reduce(p).astype(np.float64) * 0.6).astype(np.float32)
+            want, prm = oracle_step(layout, gc, s.st, s.prm, 3)
+            covered = np.zeros(n, bool)
+            for a, b in spans:
+                covered[a:b] = True
+            want = [np.where(covered, w, o) for w, o in zip(want, s.st)]
+            s.check(want, np.where(covered, prm, s.prm), f"{layout} {gdt}")
