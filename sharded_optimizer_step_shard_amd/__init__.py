@@ -158,8 +158,8 @@ def lib() -> ctypes.CDLL:
 
 def _addr(x: Ptr) -> Optional[int]:
     """Device address of a tensor (must be contiguous and on a GPU) or a raw int."""
-    if x is None:
-        return None
+    if x is None or type(x) is int:
+        return x
     if isinstance(x, (int, np.integer)):
         return int(x)
     if not x.is_cuda:
@@ -169,33 +169,40 @@ def _addr(x: Ptr) -> Optional[int]:
     return x.data_ptr()
 
 
-_raw_stream = None   # device index -> hipStream_t of torch's current stream
+_torch = _raw_stream = None   # torch, and device index -> its current stream's hipStream_t
+
+
+def _current(device: Optional[int]) -> int:
+    """The handle of torch's current stream on the current device, which has to
+    be `device` unless that is None."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _torch = torch
+        # the handle without a Stream object around it, where torch offers that
+        # (0.1 us a call against 2.7)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    here = _torch.cuda.current_device()
+    if device is not None and device != here:
+        raise ValueError(f"tensors on device {device} while device {here} is current: pass a "
+                         "stream of theirs, or make their device current")
+    return _raw_stream(here)
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        global _raw_stream
-        import torch
-        if _raw_stream is None:
-            # the handle without a Stream object around it, where torch offers that
-            # (0.1 us a call against 2.7)
-            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        return _raw_stream(torch.cuda.current_device())
+        return _current(None)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
 
 
 def _stream_here(stream, x) -> Optional[int]:
-    """_stream, for a call on tensor x: without a stream the call would go to
-    the current device's, which has to be x's."""
-    if stream is None and not isinstance(x, (int, np.integer, tuple)) and x is not None:
-        import torch
-        if x.get_device() != torch.cuda.current_device():
-            raise ValueError(f"tensors on device {x.get_device()} while device "
-                             f"{torch.cuda.current_device()} is current: pass a stream of theirs, "
-                             "or make their device current")
+    """_stream, for a call on x: without a stream the call goes to the current
+    device's, which has to be x's if x is a tensor."""
+    if stream is None:
+        return _current(x.get_device() if hasattr(x, "get_device") else None)
     return _stream(stream)
 
 
@@ -282,10 +289,10 @@ def _partial_array(partials):
 def _floats(x: Ptr, size: int, n: int, what: str) -> Optional[int]:
     """_addr of an array of n floating values of `size` bytes; of a tensor, type
     and length are checked (a call would write past the end of a short one)."""
-    if x is not None and not isinstance(x, (int, np.integer)):
-        dt = x.dtype
-        if dt.itemsize != size or not dt.is_floating_point or x.numel() < n:
-            raise ValueError(f"{what} must hold {n} values of float{8 * size}, not {x.numel()} of {dt}")
+    if x is None or isinstance(x, (int, np.integer)):
+        return _addr(x)
+    if x.element_size() != size or x.numel() < n or not x.is_floating_point():
+        raise ValueError(f"{what} must hold {n} values of float{8 * size}, not {x.numel()} of {x.dtype}")
     return _addr(x)
 
 

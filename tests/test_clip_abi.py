@@ -307,6 +307,9 @@ def test_tensors_on_a_device_that_is_not_current_are_refused(monkeypatch):
         def element_size(self):
             return 8
 
+        def is_floating_point(self):
+            return True
+
     t = On1()
     sp = zs.ClipSpec(1.0, 1e-6, 1.0, at(90))
     for call in (lambda **k: zs.zero_clip_coef(t, 4, sp, **k), lambda **k: zs.zero_scale_pieces(at(2), 1, t, **k),
@@ -339,6 +342,9 @@ def test_the_binding_refuses_arrays_of_another_type_or_size():
 
         def element_size(self):
             return self.dtype.itemsize
+
+        def is_floating_point(self):
+            return self.dtype.is_floating_point
 
     f64, f32 = (lambda n: Fake(torch.float64, n)), (lambda n: Fake(torch.float32, n))
     sp, ws = zs.ClipSpec(1.0, 1e-6, 1.0, at(90)), (at(3), 1 << 20)
